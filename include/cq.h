@@ -307,6 +307,147 @@ CQ_API cq_status cq_moe_ffn(const cq_moe_desc *d, const void *x, const float *ro
                      float *out, const cq_moe_debug *dbg, cq_stream_t stream);
 
 /*
+ * The operators between two LUT linears of a decoder layer.  Each reads the
+ * fp32 rows that cq_lut_gemm / cq_moe_ffn write and makes the fp16 rows (or
+ * the codes) that the next call reads.
+ *
+ * cq_residual_norm -- norm of a block's output, gate, residual scale, residual
+ * add and the norm before the next block, in one pass; optionally also the
+ * rotation and quantization of the result.
+ *
+ *   v  = norm(y; post_weight, post_bias) if post_norm, else y
+ *   r' = round_resid( resid_scale * r + block_scale * g * v )
+ *   x  = fp16( norm(r'; pre_weight, pre_bias) )
+ *   codes, s = cq_rotate_quantize(x, had_block, act_bits)    if act_bits > 0
+ *   norm(v; w, b) = (v - mean) / sqrt(mean((v - mean)^2) + eps) * w + b
+ *   (CQ_NORM_RMS: the means subtracted are 0 and there is no b)
+ * r' and x are evaluated in fp64 and rounded once, to nearest even, so x is
+ * the correctly rounded norm of the stored r' (up to fp64 rounding), and the
+ * codes and scales are those of cq_rotate_quantize on that x, bit for bit.
+ *
+ * y          fp32 [T, H] output of the block, or NULL: no block before this
+ *            norm.  Then r' = r, resid_out is not written (may be NULL), and
+ *            post_norm, gate_mode, resid_scale and block_scale must be 0,
+ *            CQ_GATE_NONE, 1 and 1.
+ * gate       fp16; CQ_GATE_CHANNEL [H], CQ_GATE_TOKEN [T], CQ_GATE_ELEMENT
+ *            [T, H]; NULL iff CQ_GATE_NONE (g = 1)
+ * post_weight, pre_weight  fp16 [H] or NULL (1); post_bias, pre_bias fp16 [H]
+ *            or NULL (0); biases need CQ_NORM_LAYER, the post_* pointers need
+ *            post_norm
+ * resid      [T, H], fp16 (resid_bits 16) or fp32 (32); resid_out the same
+ *            type, may be resid itself (in place)
+ * x_out      fp16 [T, H]
+ * q_out, s_out  as cq_rotate_quantize; both NULL iff act_bits = 0
+ * The outputs may not overlap each other or any input, resid_out = resid
+ * apart.  r' and x must stay inside the range of their type.
+ * Requires H % 8 == 0, 8 <= H <= 16384, T <= 2^31 - 1; T >= 0 (T = 0 is a
+ * no-op); eps > 0 and finite, scales finite; act_bits in {0, 4, 8}; with
+ * codes, had_block as cq_rotate_quantize (0 without).
+ */
+enum cq_norm_kind { CQ_NORM_RMS = 0, CQ_NORM_LAYER = 1 };
+enum cq_gate_mode {
+    CQ_GATE_NONE = 0,
+    CQ_GATE_CHANNEL = 1,
+    CQ_GATE_TOKEN = 2,
+    CQ_GATE_ELEMENT = 3
+};
+typedef struct {
+    int64_t H;
+    int32_t norm;        /* cq_norm_kind, of both norms */
+    int32_t post_norm;   /* 1: y is normed before the gate */
+    int32_t gate_mode;   /* cq_gate_mode */
+    int32_t resid_bits;  /* 16 or 32 */
+    int32_t had_block;   /* rotation block of the codes (0 without codes) */
+    int32_t act_bits;    /* 4, 8, or 0: no codes */
+    double eps;
+    double resid_scale;
+    double block_scale;
+} cq_norm_desc;
+CQ_API cq_status cq_residual_norm(const cq_norm_desc *d, int64_t T, const float *y,
+                                  const void *gate, const void *post_weight,
+                                  const void *post_bias, const void *resid, void *resid_out,
+                                  const void *pre_weight, const void *pre_bias, void *x_out,
+                                  void *q_out, float *s_out, cq_stream_t stream);
+
+/*
+ * cq_lora_add -- low-rank adapters of many requests beside a shared
+ * projection (cq_lut_gemm of the same rows):
+ *
+ *   out[m,:] = y[m,:] + scale[i] * B[i] (A[i] x[m,:]),   i = ids[m]
+ *
+ * The products of fp16 x and A are exact and summed in fp32; A x is carried
+ * with at least 20 bits relative to its row's largest entry; the sum over the
+ * rank and the addition to y are fp32.  Rows of the same adapter are worked
+ * on together, in whatever order they stand.  A row's result does not depend
+ * on the other rows' values.
+ *
+ * x        fp16 [M, K]
+ * ids      int32 [M]; a value outside [0, n_adapters) is no adapter: out = y
+ * a        fp16 [n_adapters, r_max, K]
+ * b        fp16 [n_adapters, N, r_max]
+ * scale    fp32 [n_adapters] or NULL (1)
+ * ranks    int32 [n_adapters] or NULL (r_max): the first ranks[i] rows of A[i]
+ *          and columns of B[i] are used (clamped to [0, r_max]); what the
+ *          others hold does not matter
+ * y, out   fp32 [M, N], row strides ldy, ldo (elements, >= N): slices of wider
+ *          rows are allowed.  out may be y itself (in place; ldo = ldy) and
+ *          may not overlap it otherwise.
+ * workspace  scratch of at least cq_lora_add_workspace_size(M, n_adapters)
+ *          bytes (may be NULL when that size is 0)
+ * Requires K % 8 == 0, N % 8 == 0, r_max % 8 == 0, 8 <= r_max <= 128,
+ * ldy % 4 == 0, ldo % 4 == 0, 1 <= n_adapters <= 4096, M <= 2^24,
+ * K, N <= 2^20 (else CQ_ERR_UNSUPPORTED); M >= 0 (M = 0 is a no-op).
+ */
+CQ_API size_t cq_lora_add_workspace_size(int64_t M, int64_t n_adapters);
+CQ_API cq_status cq_lora_add(const void *x, const int32_t *ids, int64_t M, int64_t K,
+                             const void *a, const void *b, const float *scale,
+                             const int32_t *ranks, int64_t n_adapters, int64_t r_max,
+                             const float *y, int64_t ldy, float *out, int64_t ldo, int64_t N,
+                             void *workspace, size_t workspace_bytes, cq_stream_t stream);
+
+/*
+ * cq_rope_qkv -- rotary positions on the rows of a fused QKV projection.
+ * Row m of qkv is [q heads | k heads | v heads], (n_q + 2 n_kv) * head_dim
+ * fp32 values (cq_lut_gemm's output).  Per token and head:
+ *
+ *   q, k: t = t / sqrt(mean(t^2) + eps) * weight      if q_weight / k_weight
+ *   q, k: pair i < rot_dim / 2 of the first rot_dim channels is turned by
+ *         positions[m] * inv_freq[i]:
+ *           (a, b) -> attn_scale * (a cos - b sin, a sin + b cos)
+ *         pairs (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved; the other
+ *         channels are kept
+ *   v:    kept
+ * and rounded to fp16.  The angle is formed and reduced in fp64 (any int32
+ * position), the rest is fp32.
+ *
+ * qkv        fp32 [M, (n_q + 2 n_kv) * head_dim]
+ * positions  int32 [M]
+ * inv_freq   fp32 [rot_dim / 2] (NULL iff rot_dim = 0)
+ * q_weight, k_weight  fp16 [head_dim] or NULL (no norm)
+ * q_out      fp16 [M, n_q, head_dim]
+ * k_out, v_out  fp16; token row t, head h at t * kv_token_stride +
+ *            h * kv_head_stride (elements).  t = m, or slots[m].
+ * slots      int64 [M] or NULL: the cache row of each token.  The k and v of a
+ *            token whose slot is outside [0, n_slots) are not written.  If two
+ *            tokens have the same slot, its contents are unspecified.
+ * Requires head_dim % 8 == 0, 8 <= head_dim <= 256, rot_dim % 8 == 0,
+ * 0 <= rot_dim <= head_dim, n_q >= 1, n_kv >= 1, n_q + 2 n_kv <= 1024, strides
+ * multiples of 8 and >= 0, M <= 2^31 - 1 (M = 0 is a no-op), eps > 0.
+ */
+typedef struct {
+    int64_t n_q, n_kv, head_dim, rot_dim;
+    int64_t kv_token_stride, kv_head_stride;
+    int64_t n_slots;      /* token rows of k_out and v_out (used with slots) */
+    int32_t interleaved;
+    float attn_scale;
+    float eps;
+} cq_rope_desc;
+CQ_API cq_status cq_rope_qkv(const cq_rope_desc *d, int64_t M, const float *qkv,
+                             const int32_t *positions, const float *inv_freq,
+                             const void *q_weight, const void *k_weight, void *q_out,
+                             void *k_out, void *v_out, const int64_t *slots, cq_stream_t stream);
+
+/*
  * Measurement aids (not part of the layer's computation).
  *
  * cq_launch_count   number of kernels this library has launched since it was
@@ -340,7 +481,10 @@ enum cq_kernel_kind {
     CQ_KERNEL_ROUTE = 6,           /* router top-k and expert grouping (two kernels) */
     CQ_KERNEL_COMBINE = 7,         /* weighted sum of expert outputs */
     CQ_KERNEL_REDUCE = 8,          /* split-K partial sums -> y */
-    CQ_KERNEL_CENTROID_SUMS = 9    /* per-centroid integer sums */
+    CQ_KERNEL_CENTROID_SUMS = 9,   /* per-centroid integer sums */
+    CQ_KERNEL_RESIDUAL_NORM = 10,  /* norms, gate, residual (and codes) */
+    CQ_KERNEL_LORA_ADD = 11,       /* low-rank adapters */
+    CQ_KERNEL_ROPE_QKV = 12        /* rotary positions and cache rows */
 };
 CQ_API int64_t cq_launch_count(void);
 
