@@ -27,37 +27,52 @@ struct NormArgs {
     uint8_t *q;
     float *s;
     int64_t ldq, T;
-    double eps, resid_scale, block_scale;
+    double eps, resid_scale, block_scale, inv_h;
     int H, layer, post_norm, gate_mode, bits, log2b;
     int tpr, rpc;  // threads per row (a multiple of 32), rows per CTA
 };
 
-// A row's threads hold it in registers, E consecutive channels each, and share
-// sums and the exchange area of the rotation through shared memory.
+// Threads of a row.  Sums go through shared memory; the half of the
+// buffer alternates, so that one barrier a sum is enough.
 struct RowThreads {
-    int row, j;       // row of the CTA, thread of the row
+    int j;            // thread of the row
     int warps, warp0; // warps of a row, first warp of this row
-    double *red;      // [2][32], the half alternates so that one barrier a sum is enough
+    double *red;      // [2][32]
     int flip;
 };
 
-template <bool MAX>
-CQ_DEV double row_reduce(double v, RowThreads &rt) {
+CQ_DEV double row_sum(double v, RowThreads &rt) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const double u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmax(v, u) : v + u;
-    }
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     double *red = rt.red + 32 * rt.flip;
     rt.flip ^= 1;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     v = red[rt.warp0];
-    for (int w = 1; w < rt.warps; w++) v = MAX ? fmax(v, red[rt.warp0 + w]) : v + red[rt.warp0 + w];
+#pragma unroll 4
+    for (int w = 1; w < rt.warps; w++) v += red[rt.warp0 + w];
     return v;
 }
 
-// 8 fp16 values as fp64
+// fp16 -> fp64 without the conversion unit, which does 16 lanes a cycle where
+// fp64 is involved: the fp16 bits are put at the top of an fp64 word by two or
+// three integer instructions (sign in place, exponent and mantissa below a
+// field of zeros).  That is the value times 2^-1008, exactly, zeros and
+// subnormals included (they are fp64 subnormals of the same pattern).
+constexpr double kHalfUp = 0x1p1008;
+CQ_DEV double half_tiny(int top) {  // fp16 in the upper half of top
+    return __hiloint2double((top >> 6) & 0x81fffc00, 0);
+}
+// 8 fp16 values, times 2^-1008
+CQ_DEV void halves_tiny(const uint4 &u, double *v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[2 * i] = half_tiny((int)(w[i] << 16));
+        v[2 * i + 1] = half_tiny((int)w[i]);
+    }
+}
+// 8 fp16 values through fp32 (the conversion unit has room for some)
 CQ_DEV void halves(const uint4 &u, double *v) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&u);
 #pragma unroll
@@ -68,35 +83,52 @@ CQ_DEV void halves(const uint4 &u, double *v) {
     }
 }
 
-// v = norm(v) over the row; nv of the thread's E channels exist (0 beyond).
+// v = norm(v) over the row; nv of the thread's E channels exist, the others are
+// 0 and stay 0.
 template <int E>
 CQ_DEV void norm_regs(double (&v)[E], int nv, const NormArgs &a, const __half *w, const __half *b,
                       int c0, RowThreads &rt) {
-    const double n = (double)a.H;
     if (a.layer) {
-        double t = 0.0;
+        double t = 0.0, u = 0.0;
 #pragma unroll
-        for (int i = 0; i < E; i++) t += v[i];
-        const double mean = row_reduce<false>(t, rt) / n;
+        for (int i = 0; i < E; i += 2) {
+            t += v[i];
+            u += v[i + 1];
+        }
+        const double mean = row_sum(t + u, rt) * a.inv_h;
 #pragma unroll
-        for (int i = 0; i < E; i++) v[i] = i < nv ? v[i] - mean : 0.0;
+        for (int c = 0; c < E; c += 8)
+            if (c < nv) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[c + i] -= mean;
+            }
     }
-    double t = 0.0;
+    uint4 wv[E / 8];
+    if (w) {
 #pragma unroll
-    for (int i = 0; i < E; i++) t = fma(v[i], v[i], t);
-    const double inv = 1.0 / sqrt(row_reduce<false>(t, rt) / n + a.eps);
+        for (int c = 0; c < E / 8; c++)
+            wv[c] = 8 * c < nv ? *reinterpret_cast<const uint4 *>(w + c0 + 8 * c) : make_uint4(0, 0, 0, 0);
+    }
+    double t = 0.0, u = 0.0;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+        t = fma(v[i], v[i], t);
+        u = fma(v[i + 1], v[i + 1], u);
+    }
+    const double inv = rsqrt(fma(row_sum(t + u, rt), a.inv_h, a.eps));
 #pragma unroll
     for (int c = 0; c < E; c += 8) {
-        double f[8];
-        if (c < nv && w) {
-            halves(*reinterpret_cast<const uint4 *>(w + c0 + c), f);
+        if (w) {
+            double f[8];
+            halves(wv[c / 8], f);
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c + i] *= inv * f[i];
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c + i] *= inv;
         }
-        if (c < nv && b) {
+        if (b && c < nv) {
+            double f[8];
             halves(*reinterpret_cast<const uint4 *>(b + c0 + c), f);
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c + i] += f[i];
@@ -104,11 +136,11 @@ CQ_DEV void norm_regs(double (&v)[E], int nv, const NormArgs &a, const __half *w
     }
 }
 
-// N butterfly levels over 2^N registers at v[0 .. 2^N)
-template <int N>
+// Butterfly levels [L0, N) over 2^N registers at v[0 .. 2^N)
+template <int N, int L0 = 0>
 CQ_DEV void butterflies(double *v) {
 #pragma unroll
-    for (int h = 1; h < (1 << N); h <<= 1)
+    for (int h = 1 << L0; h < (1 << N); h <<= 1)
 #pragma unroll
         for (int i = 0; i < (1 << N); i++)
             if ((i & h) == 0) {
@@ -117,111 +149,189 @@ CQ_DEV void butterflies(double *v) {
                 v[i + h] = x - y;
             }
 }
-
-template <int E>
-struct Log2;
-template <>
-struct Log2<16> {
-    static constexpr int v = 4;
-};
-template <>
-struct Log2<32> {
-    static constexpr int v = 5;
-};
-
-// Place of position p in the exchange area: one double of padding per E, so
-// that threads writing E consecutive positions each hit different banks.
-template <int E>
-CQ_DEV int xplace(int p) {
-    return p + (p >> Log2<E>::v);
+// Levels [0, N) of values that are 2^-1008 of theirs: the first level scales.
+template <int E, int N>
+CQ_DEV void first_levels(double (&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+        if (N == 0) {
+            v[i] *= kHalfUp;
+            v[i + 1] *= kHalfUp;
+        } else {
+            const double y = v[i + 1] * kHalfUp;
+            v[i + 1] = fma(v[i], kHalfUp, -y);
+            v[i] = fma(v[i], kHalfUp, y);
+        }
+    }
+    if (N > 1) {
+#pragma unroll
+        for (int i = 0; i < E; i += 1 << N) butterflies<N, 1>(v + i);
+    }
 }
 
-// Position of register i of thread j in the stage that works on index bits
-// [s, s + N): column c = j + (i >> N) * T of the row's H / 2^N columns, its
-// element i & (2^N - 1).
+// f(Int<n>) for n in [N, MAX]
 template <int N>
-CQ_DEV int xpos(int i, int j, int T, int s) {
-    const int c = j + (i >> N) * T;
-    return ((c >> s) << (s + N)) + ((i & ((1 << N) - 1)) << s) + (c & ((1 << s) - 1));
-}
-
-template <int E, int N>
-CQ_DEV void stage(double (&v)[E], double *xch, int j, int T, int s, bool last) {
-#pragma unroll
-    for (int i = 0; i < E; i++) v[i] = xch[xplace<E>(xpos<N>(i, j, T, s))];
-#pragma unroll
-    for (int i = 0; i < E; i += 1 << N) butterflies<N>(v + i);
-    if (!last) {
-#pragma unroll
-        for (int i = 0; i < E; i++) xch[xplace<E>(xpos<N>(i, j, T, s))] = v[i];
+struct Int {
+    static constexpr int v = N;
+};
+template <int N, int MAX, class F>
+CQ_DEV void with_const(int n, F &&f) {
+    if constexpr (N < MAX) {
+        if (n == N)
+            f(Int<N>{});
+        else
+            with_const<N + 1, MAX>(n, f);
+    } else {
+        f(Int<MAX>{});
     }
 }
 
-template <int E, int N>
-CQ_DEV void put_codes(const double (&v)[E], int8_t *cb, int j, int T, int s, double R, long long Ai,
-                      int qmax) {
+constexpr int log2_of(int e) { return e <= 1 ? 0 : 1 + log2_of(e / 2); }
+
+// The exchange area holds position p of a row at p + p / E: one double of
+// padding per E, so that threads writing E consecutive positions each hit
+// different banks.  In the stage of index bits [S, S + N) (S >= log2 E) a thread
+// holds columns c = j + k T of the row's H / 2^N, 2^N positions each, 2^S apart;
+// T threads of a row have channels.
+template <int E, int S, int N>
+struct Stage {
+    static constexpr int LE = log2_of(E);
+    static constexpr int step = (1 << S) + (1 << (S - LE));  // places between a column's positions
+    CQ_DEV static int place(int c) {
+        const int hi = c >> S, lo = c & ((1 << S) - 1);
+        return hi * (step << N) + lo + (lo >> LE);
+    }
+    CQ_DEV static int position(int c) { return ((c >> S) << (S + N)) + (c & ((1 << S) - 1)); }
+
+    CQ_DEV static void run(double (&v)[E], double *xch, int j, int T, bool store) {
 #pragma unroll
-    for (int i = 0; i < E; i++) {
-        // round(v R) to even by adding 1.5 * 2^52; within 5e-7 of a tie the exact
-        // rational decides
-        const double big = fma(v[i], R, 6755399441055744.0);
-        const double r = fma(v[i], R, -(big - 6755399441055744.0));
-        int c = __double2loint(big);
-        if ((__double2hiint(r) & 0x7fffffff) >= 0x3fdffffe) c = quantize_tie(v[i], Ai, qmax);
-        cb[N ? xpos<N>(i, j, T, s) : E * j + i] = (int8_t)c;
+        for (int k = 0; k < (E >> N); k++) {
+            double *col = xch + place(j + k * T);
+#pragma unroll
+            for (int m = 0; m < (1 << N); m++) v[(k << N) + m] = col[m * step];
+            butterflies<N>(v + (k << N));
+            if (store) {
+#pragma unroll
+                for (int m = 0; m < (1 << N); m++) col[m * step] = v[(k << N) + m];
+            }
+        }
+    }
+};
+
+// The groups of index bits from S up, each ending in the exchange area.
+template <int E, int S>
+CQ_DEV void upper_groups(double (&v)[E], double *xch, int j, int T, int lb, bool mine) {
+    constexpr int kTop = 13, LE = log2_of(E);  // blocks of at most 2^13
+    if constexpr (S < kTop) {
+        if (lb <= S) return;
+        constexpr int NMAX = kTop - S < LE ? kTop - S : LE;
+        if (mine)
+            with_const<1, NMAX>(min(lb - S, LE),
+                                [&](auto N) { Stage<E, S, N.v>::run(v, xch, j, T, true); });
+        __syncthreads();
+        upper_groups<E, S + LE>(v, xch, j, T, lb, mine);
     }
 }
 
-// 16 code bytes -> 8 bytes of nibbles, low nibble first
-CQ_DEV uint2 nibbles(const uint4 &u) {
-    auto pack = [](uint32_t a, uint32_t b) {
-        a &= 0x0f0f0f0fu;
-        b &= 0x0f0f0f0fu;
-        a |= a >> 4;
-        b |= b >> 4;
-        return prmt(a, b, 0x6420);
-    };
-    return make_uint2(pack(u.x, u.y), pack(u.z, u.w));
+// 1 / A to about 1e-14 (A a positive rotated value: 2^-24 to 2^29): fp32, then
+// one Newton step.  The codes need it to 1e-9 (see round_code).
+CQ_DEV double recip(double A) {
+    const double r = (double)(1.0f / (float)A);
+    return r * fma(-A, r, 2.0);
+}
+
+// Code of a value: v R rounded to even by adding 1.5 * 2^52; within 5e-7 of a tie
+// (near) the exact rational decides instead.
+constexpr double kMagic = 6755399441055744.0;
+CQ_DEV int round_code(double v, double R, bool &near) {
+    const double big = fma(v, R, kMagic);
+    const double r = fma(v, R, kMagic - big);
+    near = (__double2hiint(r) & 0x7fffffff) >= 0x3fdffffe;
+    return __double2loint(big);
+}
+
+// Writes the codes of a column of 2^N values 2^LE positions apart.
+template <int E, int N>
+CQ_DEV void put_columns(const double (&v)[E], int8_t *cb, int j, int T, double R, long long Ai,
+                        int qmax) {
+    constexpr int LE = log2_of(E);
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < (E >> N); k++) {
+        int8_t *col = cb + Stage<E, LE, N>::position(j + k * T);
+#pragma unroll
+        for (int m = 0; m < (1 << N); m++) {
+            bool near;
+            col[m << LE] = (int8_t)round_code(v[(k << N) + m], R, near);
+            any = any || near;
+        }
+    }
+    if (any) {
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+            bool near;
+            round_code(v[i], R, near);
+            if (near)
+                cb[Stage<E, LE, N>::position(j + (i >> N) * T) + ((i & ((1 << N) - 1)) << LE)] =
+                    (int8_t)quantize_tie(v[i], Ai, qmax);
+        }
+    }
+}
+
+// 4 codes as bytes -> nibbles 0-3 in bits 0-15 (low nibble first)
+CQ_DEV uint32_t nibbles(uint32_t a) {
+    a &= 0x0f0f0f0fu;
+    return a | a >> 4;  // bytes 0 and 2 hold the pairs
 }
 
 // Rows in registers, E channels a thread.  The rotation's index bits are taken
-// log2 E at a time: the first in the layout of the loads, each further group
+// log2 E at a time: the lowest in the layout of the loads, each further group
 // after an exchange through shared memory that puts the group's 2^N values into
 // one thread (2 shared accesses a value for up to log2 E levels; a lane shuffle
-// of an fp64 value costs 2 instructions a level).  Codes go through shared
-// memory once, as bytes, back to the layout of the loads.
+// of an fp64 value costs 2 instructions a level).  The groups above the second
+// come first and the second, [log2 E, ..), last, so the codes are made in one of
+// few layouts; they go through shared memory once, as bytes, back to the layout
+// of the loads.
 template <int E, bool R16, bool CODES>
-__global__ void __launch_bounds__(512) k_residual_norm(const NormArgs a) {
+__global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(const NormArgs a) {
     extern __shared__ __align__(16) double xch_all[];
     __shared__ double red[64];
-    constexpr int LE = Log2<E>::v;
+    __shared__ int s_hi[16];
+    __shared__ unsigned s_lo[16];
+    constexpr int LE = log2_of(E);
+    constexpr int RS = R16 ? E / 8 : E / 4;  // 16-byte pieces of a thread's residual
     griddep_wait();
     griddep_launch();
     RowThreads rt;
-    rt.row = threadIdx.x / a.tpr;
-    rt.j = threadIdx.x - rt.row * a.tpr;
+    const int row = threadIdx.x / a.tpr;
+    rt.j = threadIdx.x - row * a.tpr;
     rt.warps = a.tpr >> 5;
-    rt.warp0 = rt.row * rt.warps;
+    rt.warp0 = row * rt.warps;
     rt.red = red;
     rt.flip = 0;
+    if (threadIdx.x < 16) {  // in use after the barriers of the sums
+        s_hi[threadIdx.x] = 0;
+        s_lo[threadIdx.x] = 0;
+    }
     const int H = a.H, j = rt.j, c0 = E * j;
-    const int64_t t = (int64_t)blockIdx.x * a.rpc + rt.row;
+    const int T = H / E;  // threads of the row with channels, where blocks go over E channels
+    double *xch = xch_all + (size_t)row * (H + T);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int64_t t = (int64_t)blockIdx.x * a.rpc + row;
     const int nv = t < a.T ? max(0, min(E, H - c0)) : 0;  // a multiple of 8
     const int64_t at = t * H + c0;
 
     double v[E];
-#pragma unroll
-    for (int i = 0; i < E; i++) v[i] = 0.0;
     // everything the row reads once is requested before the first use
-    uint4 rr[R16 ? E / 8 : E / 4];
+    uint4 rr[RS];
     if (R16) {
         const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const __half *>(a.resid) + at);
 #pragma unroll
-        for (int c = 0; c < E / 8; c++) rr[c] = 8 * c < nv ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < E / 8; c++) rr[c] = 8 * c < nv ? __ldcs(src + c) : zero;
     } else {
         const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(a.resid) + at);
 #pragma unroll
-        for (int c = 0; c < E / 4; c++) rr[c] = 4 * c < nv ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < E / 4; c++) rr[c] = 4 * c < nv ? __ldcs(src + c) : zero;
     }
     if (a.y) {
         const float4 *src = reinterpret_cast<const float4 *>(a.y + at);
@@ -245,11 +355,11 @@ __global__ void __launch_bounds__(512) k_residual_norm(const NormArgs a) {
             const __half *gp = a.gate + (a.gate_mode == CQ_GATE_CHANNEL ? c0 : at);
 #pragma unroll
             for (int c = 0; c < E; c += 8) {
-                double f[8];
                 if (c < nv) {
-                    halves(*reinterpret_cast<const uint4 *>(gp + c), f);
+                    double f[8];
+                    halves_tiny(*reinterpret_cast<const uint4 *>(gp + c), f);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) v[c + i] *= f[i];
+                    for (int i = 0; i < 8; i++) v[c + i] *= f[i] * kHalfUp;
                 }
             }
         }
@@ -258,121 +368,117 @@ __global__ void __launch_bounds__(512) k_residual_norm(const NormArgs a) {
     if (R16) {
 #pragma unroll
         for (int c = 0; c < E / 8; c++) {
-            double f[8];
-            halves(rr[c], f);
             if (a.y) {
-                uint4 o;
-                __half *h = reinterpret_cast<__half *>(&o);
+                double f[8];
+                halves(rr[c], f);
+                __half2 *h = reinterpret_cast<__half2 *>(&rr[c]);
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    h[i] = __double2half(fma(a.resid_scale, f[i], a.block_scale * v[8 * c + i]));
+                for (int i = 0; i < 8; i += 2)
+                    h[i / 2] = __halves2half2(
+                        __double2half(fma(a.resid_scale, f[i], a.block_scale * v[8 * c + i])),
+                        __double2half(fma(a.resid_scale, f[i + 1], a.block_scale * v[8 * c + i + 1])));
                 if (8 * c < nv)
-                    *reinterpret_cast<uint4 *>(reinterpret_cast<__half *>(a.resid_out) + at + 8 * c) = o;
-                halves(o, f);
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<__half *>(a.resid_out) + at + 8 * c) = rr[c];
             }
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[8 * c + i] = 8 * c < nv ? f[i] : 0.0;
+            halves(rr[c], v + 8 * c);
         }
     } else {
 #pragma unroll
         for (int c = 0; c < E / 4; c++) {
-            const float *r = reinterpret_cast<const float *>(&rr[c]);
-            float4 o;
-            float *f = reinterpret_cast<float *>(&o);
+            float *f = reinterpret_cast<float *>(&rr[c]);
+            if (a.y) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                f[i] = r[i];
-                if (a.y)
+                for (int i = 0; i < 4; i++)
                     f[i] = __double2float_rn(
-                        fma(a.resid_scale, (double)r[i], a.block_scale * v[4 * c + i]));
+                        fma(a.resid_scale, (double)f[i], a.block_scale * v[4 * c + i]));
+                if (4 * c < nv)
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<float *>(a.resid_out) + at + 4 * c) = rr[c];
             }
-            if (a.y && 4 * c < nv)
-                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.resid_out) + at + 4 * c) = o;
 #pragma unroll
-            for (int i = 0; i < 4; i++) v[4 * c + i] = 4 * c < nv ? (double)f[i] : 0.0;
+            for (int i = 0; i < 4; i++) v[4 * c + i] = (double)f[i];
         }
     }
     norm_regs<E>(v, nv, a, a.pre_w, a.pre_b, c0, rt);
 #pragma unroll
     for (int c = 0; c < E / 8; c++) {
         uint4 o;
-        __half *h = reinterpret_cast<__half *>(&o);
+        __half2 *h = reinterpret_cast<__half2 *>(&o);
 #pragma unroll
-        for (int i = 0; i < 8; i++) h[i] = __double2half(v[8 * c + i]);
+        for (int i = 0; i < 8; i += 2)
+            h[i / 2] = __halves2half2(__double2half(v[8 * c + i]), __double2half(v[8 * c + i + 1]));
         if (8 * c < nv) *reinterpret_cast<uint4 *>(a.x + at + 8 * c) = o;
-        if (CODES) halves(o, v + 8 * c);
+        if (CODES) halves_tiny(o, v + 8 * c);
     }
     if (!CODES) return;
 
     // ---- rotation (channels beyond the row are zeros of whole blocks of 8)
-    switch (min(a.log2b, LE)) {
-    case 0: break;
-#define CQ_FIRST(N) \
-    case N: \
-        for (int i = 0; i < E; i += 1 << N) butterflies<N>(v + i); \
-        break;
-        CQ_FIRST(1) CQ_FIRST(2) CQ_FIRST(3) CQ_FIRST(4)
-    default:
-        if (LE == 5) butterflies<LE>(v);
-#undef CQ_FIRST
-    }
-    const int T = H / E;  // threads of the row with channels (rotation blocks over E divide H)
-    double *xch = xch_all + (size_t)rt.row * (H + T);
-    int s = 0, n = 0;  // bits [s, s + n) of the last exchange (n = 0: none)
-    if (a.log2b > LE) {
-        const bool mine = nv > 0;
+    const int lb = a.log2b;
+    with_const<0, LE>(min(lb, LE), [&](auto N) { first_levels<E, N.v>(v); });
+    const bool mine = nv > 0;
+    const int n2 = min(max(lb - LE, 0), LE);  // bits of the second group
+    if (n2 > 0) {
         if (mine) {
 #pragma unroll
-            for (int i = 0; i < E; i++) xch[xplace<E>(c0 + i)] = v[i];
+            for (int i = 0; i < E; i++) xch[(E + 1) * j + i] = v[i];
         }
-        for (s = LE; s < a.log2b; s += n) {
-            n = min(LE, a.log2b - s);
-            const bool last = s + n == a.log2b;
-            __syncthreads();
-            if (mine) {
-                switch (n) {
-                case 1: stage<E, 1>(v, xch, j, T, s, last); break;
-                case 2: stage<E, 2>(v, xch, j, T, s, last); break;
-                case 3: stage<E, 3>(v, xch, j, T, s, last); break;
-                case 4: stage<E, 4>(v, xch, j, T, s, last); break;
-                default: stage<E, LE>(v, xch, j, T, s, last); break;
-                }
-            }
-        }
-        s -= n;
+        __syncthreads();
+        upper_groups<E, 2 * LE>(v, xch, j, T, lb, mine);
+        if (mine)
+            with_const<1, LE>(n2, [&](auto N) { Stage<E, LE, N.v>::run(v, xch, j, T, false); });
     }
-    // ---- codes
-    double mx = 0.0;
+    // ---- the row's largest magnitude.  fp64 comparisons run at 16 lanes a cycle:
+    // the magnitudes are compared as integers, first the high words of all, then
+    // the low words of those whose high word is the largest
+    int mh = 0;
 #pragma unroll
-    for (int i = 0; i < E; i++) mx = fmax(mx, fabs(v[i]));
-    const double A = row_reduce<true>(mx, rt);  // its barrier also frees the exchange area
+    for (int i = 0; i < E; i++) mh = max(mh, __double2hiint(v[i]) & 0x7fffffff);
+    if (!mine) mh = 0;
+    const int wh = __reduce_max_sync(0xffffffffu, mh);
+    if ((threadIdx.x & 31) == 0) atomicMax(&s_hi[row], wh);
+    __syncthreads();  // also: the exchange area is free
+    const int top = s_hi[row];
+    if (mine && mh == top) {
+        unsigned ml = 0;
+#pragma unroll
+        for (int i = 0; i < E; i++)
+            if ((__double2hiint(v[i]) & 0x7fffffff) == top) ml = max(ml, (unsigned)__double2loint(v[i]));
+        atomicMax(&s_lo[row], ml);
+    }
+    __syncthreads();
+    const double A = __hiloint2double(top, (int)s_lo[row]);
     const int qmax = (1 << (a.bits - 1)) - 1;
     const long long Ai = __double2ll_rn(A * 16777216.0);
-    const double R = Ai > 0 ? __ddiv_rn((double)qmax, A) : 0.0;
+    const double R = Ai > 0 ? (double)qmax * recip(A) : 0.0;
+    if (j == 0 && mine) a.s[t] = Ai > 0 ? quant_scale(A, lb, qmax) : 0.0f;
     int8_t *cb = reinterpret_cast<int8_t *>(xch);
-    if (nv > 0) {
-        switch (n) {
-        case 0: put_codes<E, 0>(v, cb, j, T, s, R, Ai, qmax); break;
-        case 1: put_codes<E, 1>(v, cb, j, T, s, R, Ai, qmax); break;
-        case 2: put_codes<E, 2>(v, cb, j, T, s, R, Ai, qmax); break;
-        case 3: put_codes<E, 3>(v, cb, j, T, s, R, Ai, qmax); break;
-        case 4: put_codes<E, 4>(v, cb, j, T, s, R, Ai, qmax); break;
-        default: put_codes<E, LE>(v, cb, j, T, s, R, Ai, qmax); break;
+    if (mine) {
+        if (n2 == 0) {
+            uint32_t w[E / 4];
+#pragma unroll
+            for (int i = 0; i < E; i++) {
+                bool near;
+                int c = round_code(v[i], R, near);
+                if (near) c = quantize_tie(v[i], Ai, qmax);
+                w[i / 4] = i % 4 ? w[i / 4] | (uint32_t)(c & 255) << (8 * (i % 4)) : (uint32_t)(c & 255);
+            }
+#pragma unroll
+            for (int i = 0; i < E / 4; i++) *reinterpret_cast<uint32_t *>(cb + c0 + 4 * i) = w[i];
+        } else {
+            with_const<1, LE>(n2, [&](auto N) { put_columns<E, N.v>(v, cb, j, T, R, Ai, qmax); });
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < E; c += 8) {
-        if (c >= nv) break;
-        const uint2 u = *reinterpret_cast<const uint2 *>(cb + c0 + c);
-        if (a.bits == 8) {
-            *reinterpret_cast<uint2 *>(a.q + t * a.ldq + c0 + c) = u;
-        } else {
-            const uint2 k = nibbles(make_uint4(u.x, u.y, 0, 0));
-            *reinterpret_cast<uint32_t *>(a.q + t * a.ldq + (c0 + c) / 2) = k.x;
+    for (int i = 0; i < E; i += 8) {
+        if (i < nv) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(cb + c0 + i);
+            if (a.bits == 8)
+                *reinterpret_cast<uint2 *>(a.q + t * a.ldq + c0 + i) = u;
+            else
+                *reinterpret_cast<uint32_t *>(a.q + t * a.ldq + (c0 + i) / 2) =
+                    prmt(nibbles(u.x), nibbles(u.y), 0x6420);
         }
     }
-    if (j == 0 && nv > 0) a.s[t] = Ai > 0 ? quant_scale(A, a.log2b, qmax) : 0.0f;
 }
 
 template <int E>
@@ -390,11 +496,16 @@ static cudaError_t launch_rows(NormArgs a, bool r16, cudaStream_t st) {
                       st, 1, a);
 }
 
-// 16 channels a thread; 32 for rows over 8192, which would need blocks of more
-// than 512 threads and with them half the registers.
+// 16 channels a thread at 80 registers (more registers, fewer rows at once; 64
+// would spill).  Few rows are paced by the length of a row's instruction stream:
+// 8 channels a thread then.  Rows over 8192 take 32, for blocks of at most 512
+// threads.  4096 rows of 2048, codes: 37.5 us with 16, 41.7 with 8; one row of
+// 2560: 4.7 and 3.9.
 static cudaError_t launch_residual_norm(const NormArgs &a, bool r16, cudaStream_t st) {
     TimedScope ts(st, CQ_KERNEL_RESIDUAL_NORM);
-    return a.H <= 8192 ? launch_rows<16>(a, r16, st) : launch_rows<32>(a, r16, st);
+    if (a.H > 8192) return launch_rows<32>(a, r16, st);
+    if (a.H <= 4096 && a.T <= 2 * sm_count()) return launch_rows<8>(a, r16, st);
+    return launch_rows<16>(a, r16, st);
 }
 
 static bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -454,6 +565,7 @@ extern "C" CQ_API cq_status cq_residual_norm(const cq_norm_desc *d, int64_t T, c
     a.s = s_out;
     a.H = (int)d->H;
     a.ldq = d->H * d->act_bits / 8;
+    a.inv_h = 1.0 / (double)d->H;
     a.eps = d->eps;
     a.resid_scale = d->resid_scale;
     a.block_scale = d->block_scale;
