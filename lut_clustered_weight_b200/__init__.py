@@ -1,7 +1,9 @@
 """Python binding of the B200 CodeQuant LUT MoE linear layer (libcq_b200.so).
 
 Argument marshalling only: every step runs in the CUDA library behind the C
-ABI declared in include/cq.h.  torch supplies device memory and streams.
+ABI declared in include/cq.h.  torch supplies device memory and streams.  The
+operators that a decode step calls between its linears are marshalled by the
+CPython module _cq_bind (csrc/bind.cpp), the others by ctypes.
 There is no CPU fallback: importing this package fails if the library has not
 been built (``python lut_clustered_weight_b200/build.py``).
 """
@@ -9,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
-from functools import lru_cache
 from pathlib import Path
 
 import torch
@@ -42,6 +43,12 @@ if not LIB_PATH.exists():
                       "`python lut_clustered_weight_b200/build.py` (nvcc, sm_100a)")
 
 lib = ctypes.CDLL(str(LIB_PATH))
+if not (_PKG / "_cq_bind.so").exists():
+    raise ImportError(f"{_PKG / '_cq_bind.so'} is missing: build it with "
+                      "`python lut_clustered_weight_b200/build.py`")
+from . import _cq_bind as _bind  # noqa: E402
+
+_bind.set_error(CQError)
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 
@@ -383,46 +390,7 @@ class MoELayer:
 # the operators between two LUT linears of a decoder layer
 
 
-def _need(cond, where: str, what: str):
-    if not cond:
-        raise CQError(CQ_ERR_INVALID_ARGUMENT, f"{where}: {what}")
-
-
-def _tensor(where, name, t, dtype, shape, dev):
-    """Checks one dense operand; returns its address."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise CQError(CQ_ERR_INVALID_ARGUMENT,
-                      f"{where}: {name} must be a contiguous {dtype} tensor of shape "
-                      f"{tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _optional(where, name, t, dtype, shape, dev):
-    return None if t is None else _tensor(where, name, t, dtype, shape, dev)
-
-
-def _call(where, fn, dev, stream, *args):
-    """Runs a C entry point on the operands' device, on `stream` or that
-    device's current stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    st = _stream(stream)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, st)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, st)
-    if rc != CQ_OK:
-        raise CQError(rc, where)
-
-
 NORM_KINDS = {"rms": 0, "layer": 1}   # cq_norm_kind
-_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_ELEMENT = range(4)   # cq_gate_mode
-
-
-@lru_cache(maxsize=256)
-def _norm_desc(*fields):
-    return ctypes.byref(NormDesc(*fields))
 
 
 def cq_residual_norm(resid: torch.Tensor, y=None, *, norm: str = "rms", eps: float = 1e-6,
@@ -434,71 +402,19 @@ def cq_residual_norm(resid: torch.Tensor, y=None, *, norm: str = "rms", eps: flo
     with act_bits 4 / 8 the rotated codes of x; see include/cq.h.
 
     resid fp16 or fp32 [T, H]; y fp32 [T, H] or None (no block before this norm);
-    gate fp16 [H], [T, 1] or [T, H]; weights and biases fp16 [H].  resid_out may
-    be resid itself.  Returns (r', x), or (r', x, codes, scales)."""
-    w = "cq_residual_norm"
-    dev, dt = resid.device, resid.dtype
-    _need(dev.type == "cuda", w, "resid must be a CUDA tensor")
-    _need(resid.dim() == 2, w, "resid must be [T, H]")
-    _need(dt == torch.float16 or dt == torch.float32, w, "resid must be fp16 or fp32")
-    _need(norm in NORM_KINDS, w, f"unknown norm {norm!r}")
-    _need(act_bits in (0, 4, 8), w, "act_bits must be 0, 4 or 8")
-    shape = resid.shape
-    T, H = shape
-    f16 = torch.float16
-    p_r = _tensor(w, "resid", resid, dt, shape, dev)
-    p_y = p_ro = None
-    if y is not None:
-        p_y = _tensor(w, "y", y, torch.float32, shape, dev)
-        if resid_out is None:
-            resid_out = torch.empty_like(resid)
-        p_ro = _tensor(w, "resid_out", resid_out, dt, shape, dev)
-    else:
-        _need(resid_out is None, w, "resid_out without y")
-        resid_out = resid
-    mode, p_g = _GATE_NONE, None
-    if gate is not None:
-        mode = (_GATE_CHANNEL if gate.dim() == 1 else
-                _GATE_TOKEN if gate.shape[-1] == 1 else _GATE_ELEMENT)
-        p_g = _tensor(w, "gate", gate, f16,
-                      (None, (H,), (T, 1), shape)[mode], dev)
-    vec = (H,)
-    p_qw = _optional(w, "post_weight", post_weight, f16, vec, dev)
-    p_qb = _optional(w, "post_bias", post_bias, f16, vec, dev)
-    p_pw = _optional(w, "pre_weight", pre_weight, f16, vec, dev)
-    p_pb = _optional(w, "pre_bias", pre_bias, f16, vec, dev)
-    if x_out is None:
-        x_out = torch.empty(shape, dtype=f16, device=dev)
-    p_x = _tensor(w, "x_out", x_out, f16, shape, dev)
-    p_q = p_s = None
-    if act_bits:
-        if q_out is None:
-            q_out = _empty_codes(T, H, act_bits, dev)
-        if s_out is None:
-            s_out = torch.empty((T,), dtype=torch.float32, device=dev)
-        p_q = _tensor(w, "q_out", q_out, torch.uint8 if act_bits == 4 else torch.int8,
-                      (T, code_bytes(H, act_bits)), dev)
-        p_s = _tensor(w, "s_out", s_out, torch.float32, (T,), dev)
-    else:
-        _need(q_out is None and s_out is None, w, "q_out / s_out without act_bits")
-    desc = _norm_desc(H, NORM_KINDS[norm], int(post_norm), mode, 16 if dt == f16 else 32,
-                      had_block, act_bits, eps, resid_scale, block_scale)
-    _call(w, lib.cq_residual_norm, dev, stream, desc, T, p_y, p_g, p_qw, p_qb, p_r, p_ro, p_pw,
-          p_pb, p_x, p_q, p_s)
-    return (resid_out, x_out, q_out, s_out) if act_bits else (resid_out, x_out)
+    norm "rms" or "layer"; gate fp16 [H], [T, 1] or [T, H]; weights and biases
+    fp16 [H].  resid_out may be resid itself.  Returns (r', x), or (r', x, codes,
+    scales)."""
+    kind = NORM_KINDS.get(norm)
+    if kind is None:
+        raise CQError(CQ_ERR_INVALID_ARGUMENT, f"cq_residual_norm: unknown norm {norm!r}")
+    return _bind.residual_norm(resid, y, kind, eps, pre_weight, pre_bias, post_norm, post_weight,
+                               post_bias, gate, resid_scale, block_scale, had_block, act_bits,
+                               resid_out, x_out, q_out, s_out, stream)
 
 
 def cq_lora_add_workspace_size(M: int, n_adapters: int) -> int:
     return int(lib.cq_lora_add_workspace_size(M, n_adapters))
-
-
-def _rows(where, name, t, shape, dev):
-    """An fp32 [M, N] operand whose rows may be slices of wider ones: (address,
-    row stride)."""
-    _need(t.dtype == torch.float32 and t.shape == shape and t.device == dev and
-          t.stride(1) == 1, where,
-          f"{name} must be fp32 {tuple(shape)} on {dev} with contiguous rows")
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
 
 
 def cq_lora_add(x: torch.Tensor, ids: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -507,43 +423,8 @@ def cq_lora_add(x: torch.Tensor, ids: torch.Tensor, a: torch.Tensor, b: torch.Te
     """out[m] = y[m] + scale[i] * B[i] (A[i] x[m]) with i = ids[m]; rows whose id
     is outside [0, n) keep y.  x fp16 [M, K], ids int32 [M], a fp16 [n, r, K],
     b fp16 [n, N, r], scale fp32 [n], ranks int32 [n]; y and out fp32 [M, N],
-    column slices allowed; out None: in place.  See include/cq.h."""
-    w = "cq_lora_add"
-    dev = x.device
-    _need(dev.type == "cuda", w, "x must be a CUDA tensor")
-    _need(x.dim() == 2 and a.dim() == 3 and b.dim() == 3 and y.dim() == 2, w,
-          "x [M, K], a [n, r, K], b [n, N, r], y [M, N]")
-    M, K = x.shape
-    n, r, _ = a.shape
-    N = b.shape[1]
-    f16 = torch.float16
-    p_x = _tensor(w, "x", x, f16, (M, K), dev)
-    p_i = _tensor(w, "ids", ids, torch.int32, (M,), dev)
-    p_a = _tensor(w, "a", a, f16, (n, r, K), dev)
-    p_b = _tensor(w, "b", b, f16, (n, N, r), dev)
-    p_sc = _optional(w, "scale", scale, torch.float32, (n,), dev)
-    p_rk = _optional(w, "ranks", ranks, torch.int32, (n,), dev)
-    p_y, ldy = _rows(w, "y", y, (M, N), dev)
-    if out is None:
-        out, p_o, ldo = y, p_y, ldy
-    else:
-        p_o, ldo = _rows(w, "out", out, (M, N), dev)
-    nb = lib.cq_lora_add_workspace_size(M, n)
-    if workspace is None and nb:
-        workspace = torch.empty((nb,), dtype=torch.uint8, device=dev)
-    p_w, wb = None, 0
-    if workspace is not None:
-        _need(workspace.device == dev and workspace.is_contiguous(), w,
-              f"workspace must be contiguous on {dev}")
-        p_w, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(w, lib.cq_lora_add, dev, stream, p_x, p_i, M, K, p_a, p_b, p_sc, p_rk, n, r, p_y, ldy,
-          p_o, ldo, N, p_w, wb)
-    return out
-
-
-@lru_cache(maxsize=256)
-def _rope_desc(*fields):
-    return ctypes.byref(RopeDesc(*fields))
+    column slices allowed; out None: in place.  Returns out.  See include/cq.h."""
+    return _bind.lora_add(x, ids, a, b, y, scale, ranks, out, workspace, stream)
 
 
 def cq_rope_qkv(qkv: torch.Tensor, positions: torch.Tensor, inv_freq, n_q: int, n_kv: int, *,
@@ -557,41 +438,5 @@ def cq_rope_qkv(qkv: torch.Tensor, positions: torch.Tensor, inv_freq, n_q: int, 
     rotation).  q_out [M, n_q, head_dim]; k_out, v_out [rows, n_kv, head_dim] with
     the same strides, channels contiguous: row m, or with slots (int64 [M]) row
     slots[m] of a cache, out-of-range slots not written.  Returns (q, k, v)."""
-    w = "cq_rope_qkv"
-    dev = qkv.device
-    _need(dev.type == "cuda", w, "qkv must be a CUDA tensor")
-    _need(qkv.dim() == 2, w, "qkv must be [M, (n_q + 2 n_kv) * head_dim]")
-    _need(n_q > 0 and n_kv > 0 and head_dim > 0, w, "n_q, n_kv, head_dim must be positive")
-    M = qkv.shape[0]
-    f16 = torch.float16
-    p_in = _tensor(w, "qkv", qkv, torch.float32, (M, (n_q + 2 * n_kv) * head_dim), dev)
-    p_pos = _tensor(w, "positions", positions, torch.int32, (M,), dev)
-    rot, p_f = 0, None
-    if inv_freq is not None:
-        _need(inv_freq.dim() == 1 and inv_freq.numel() > 0, w, "inv_freq must be [rot_dim / 2]")
-        rot = 2 * inv_freq.shape[0]
-        p_f = _tensor(w, "inv_freq", inv_freq, torch.float32, (rot // 2,), dev)
-    p_qw = _optional(w, "q_weight", q_weight, f16, (head_dim,), dev)
-    p_kw = _optional(w, "k_weight", k_weight, f16, (head_dim,), dev)
-    p_sl = _optional(w, "slots", slots, torch.int64, (M,), dev)
-    if q_out is None:
-        q_out = torch.empty((M, n_q, head_dim), dtype=f16, device=dev)
-    p_q = _tensor(w, "q_out", q_out, f16, (M, n_q, head_dim), dev)
-    if k_out is None and v_out is None:
-        _need(slots is None, w, "slots need k_out and v_out")
-        k_out = torch.empty((M, n_kv, head_dim), dtype=f16, device=dev)
-        v_out = torch.empty_like(k_out)
-    _need(k_out is not None and v_out is not None, w, "k_out and v_out come together")
-    st = k_out.stride()
-    _need(k_out.dtype == f16 and v_out.dtype == f16 and k_out.dim() == 3 and
-          k_out.shape == v_out.shape and st == v_out.stride() and k_out.device == dev and
-          v_out.device == dev, w, f"k_out and v_out must be fp16 on {dev}, alike in shape and strides")
-    rows = k_out.shape[0]
-    _need(k_out.shape[1] == n_kv and k_out.shape[2] == head_dim and st[2] == 1, w,
-          "k_out must be [rows, n_kv, head_dim] with contiguous channels")
-    _need(slots is not None or rows >= M, w, "k_out has fewer rows than qkv")
-    desc = _rope_desc(n_q, n_kv, head_dim, rot, st[0], st[1], rows, int(interleaved), attn_scale,
-                      eps)
-    _call(w, lib.cq_rope_qkv, dev, stream, desc, M, p_in, p_pos, p_f, p_qw, p_kw, p_q,
-          k_out.data_ptr(), v_out.data_ptr(), p_sl)
-    return q_out, k_out, v_out
+    return _bind.rope_qkv(qkv, positions, inv_freq, n_q, n_kv, head_dim, interleaved, attn_scale,
+                          q_weight, k_weight, eps, q_out, k_out, v_out, slots, stream)

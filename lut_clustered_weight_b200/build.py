@@ -1,4 +1,5 @@
-"""Build the sm_100a CUDA library in-tree: lut_clustered_weight_b200/libcq_b200.so.
+"""Build the sm_100a CUDA library in-tree: lut_clustered_weight_b200/libcq_b200.so,
+and the CPython module _cq_bind.so (tensor checks of some entry points) beside it.
 
     python lut_clustered_weight_b200/build.py [--force] [-v] [--ptxas-info]
 
@@ -10,10 +11,12 @@ one shared library whose exported symbols are the C ABI of include/cq.h.
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -22,6 +25,8 @@ CSRC = PKG / "csrc"
 INCLUDE = PKG.parent / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libcq_b200.so"
+BIND_SRC = CSRC / "bind.cpp"
+BIND = PKG / "_cq_bind.so"
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -33,6 +38,19 @@ def nvcc() -> str:
         if c and Path(c).exists():
             return c
     raise RuntimeError("nvcc not found: the CUDA library cannot be built")
+
+
+def _bind_cmd(out: Path) -> list[str]:
+    """g++ command of the CPython module: torch's headers and libraries (found
+    without importing torch), and the CUDA library beside it."""
+    torch = Path(importlib.util.find_spec("torch").submodule_search_locations[0])
+    cuda = Path(nvcc()).resolve().parent.parent
+    inc = [torch / "include", torch / "include/torch/csrc/api/include", cuda / "include",
+           sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            *[f"-isystem{i}" for i in inc], str(BIND_SRC), "-o", str(out), f"-L{PKG}",
+            "-l:libcq_b200.so", "-Wl,-rpath,$ORIGIN", f"-L{torch / 'lib'}", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _sources():
@@ -74,6 +92,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [nvcc(), *ARCH, "-shared", "-o", str(tmp), *map(str, objs), "-lcudart"]
         run(cmd)
         os.replace(tmp, LIB)
+    newest = max(p.stat().st_mtime for p in (BIND_SRC, INCLUDE / "cq.h"))
+    if force or not BIND.exists() or BIND.stat().st_mtime < newest:
+        tmp = PKG / f"._cq_bind.{os.getpid()}.so"
+        run(_bind_cmd(tmp))
+        os.replace(tmp, BIND)
     return LIB
 
 

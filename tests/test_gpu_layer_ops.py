@@ -531,3 +531,49 @@ def test_calls_are_counted_and_timed_by_kind(cq):
     assert cq.cq_launch_count() - before >= 4
     for k in ("residual_norm", "lora_add", "rope_qkv"):
         assert k in kinds
+
+
+@pytest.mark.parametrize("M", [3, 700])
+def test_calls_on_a_given_stream(cq, M):
+    """stream= takes a torch stream or its address; what the call allocates belongs
+    to that stream, so its memory is not handed to another one's work too early."""
+    A = _Layer(cq, M, seed=4)
+    want = [t.clone() for t in A.run()]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for st in (s, s.cuda_stream):
+        for _ in range(3):
+            got = A.run(stream=st)
+            junk = torch.full((M * 2048,), float("nan"), device=DEV)   # current stream's memory
+            del junk
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    with pytest.raises(AttributeError):
+        cq.cq_residual_norm(A.t["nresid"], stream="no stream")
+
+
+def test_refusals_name_the_call_and_the_operand(cq):
+    h = torch.zeros((2, 64), dtype=torch.float16, device=DEV)
+    y = torch.zeros((2, 64), device=DEV)
+    w = torch.zeros(64, dtype=torch.float16, device=DEV)
+    for kw, word in ((dict(y=y.half()), "y"), (dict(y=y[:1]), "y"), (dict(pre_weight=w.float()), "pre_weight"),
+                     (dict(y=y, gate=w[:32]), "gate"), (dict(x_out=h.t()), "x_out"),
+                     (dict(q_out=h), "act_bits"), (dict(act_bits=3), "act_bits"),
+                     (dict(resid_out=h), "resid_out"), (dict(norm="batch"), "norm"),
+                     (dict(y=y, post_weight=w), ""), (dict(pre_bias=w), ""),
+                     (dict(act_bits=4, had_block=3), ""), (dict(eps=0.0), ""),
+                     (dict(y=y, x_out=h), ""), (dict(pre_weight=w.cpu()), "pre_weight"),
+                     (dict(pre_weight=3), "pre_weight")):
+        with pytest.raises(cq.CQError) as e:
+            cq.cq_residual_norm(h, **kw)
+        assert e.value.status in (cq.CQ_ERR_INVALID_ARGUMENT, cq.CQ_ERR_UNSUPPORTED)
+        assert "cq_residual_norm" in str(e.value) and word in str(e.value)
+    with pytest.raises(cq.CQError):
+        cq.cq_residual_norm(h[:, :32])                       # rows of a wider tensor
+    with pytest.raises(cq.CQError):
+        cq.cq_residual_norm(torch.zeros((2, 12), dtype=torch.float16, device=DEV))
+    with pytest.raises(TypeError):
+        cq.cq_residual_norm(h, eps="small")
+    r, x = cq.cq_residual_norm(h)
+    assert r is h and (x == 0).all()
