@@ -243,6 +243,11 @@ LORA_CASES = [
     (1100, 640, 512, 8, 64, "runs", False),
     (1500, 136, 72, 4096, 8, "rows", False),       # the largest bank
     (2100, 256, 264, 3, 128, "rows", True),
+    (256, 64, 40, 300, 16, "rows", False),         # one row a thread of the tile search
+    (255, 40, 24, 2, 24, "none", False),
+    (2048, 96, 72, 2, 16, "none", True),
+    (9000, 16, 24, 5, 8, "rows", False),           # more rows than the sorting CTA holds
+    (17000, 8, 8, 1100, 8, "rows", True),
 ]
 
 
