@@ -392,13 +392,13 @@ CQ_API cq_status cq_residual_norm(const cq_norm_desc *d, int64_t T, const float 
  * y, out   fp32 [M, N], row strides ldy, ldo (elements, >= N): slices of wider
  *          rows are allowed.  out may be y itself (in place; ldo = ldy) and
  *          may not overlap it otherwise.
- * workspace  scratch of at least cq_lora_add_workspace_size(M, n_adapters)
+ * workspace  scratch of at least cq_lora_add_workspace_size(M, n_adapters, r_max)
  *          bytes (may be NULL when that size is 0)
  * Requires K % 8 == 0, N % 8 == 0, r_max % 8 == 0, 8 <= r_max <= 128,
  * ldy % 4 == 0, ldo % 4 == 0, 1 <= n_adapters <= 4096, M <= 2^24,
  * K, N <= 2^20 (else CQ_ERR_UNSUPPORTED); M >= 0 (M = 0 is a no-op).
  */
-CQ_API size_t cq_lora_add_workspace_size(int64_t M, int64_t n_adapters);
+CQ_API size_t cq_lora_add_workspace_size(int64_t M, int64_t n_adapters, int64_t r_max);
 CQ_API cq_status cq_lora_add(const void *x, const int32_t *ids, int64_t M, int64_t K,
                              const void *a, const void *b, const float *scale,
                              const int32_t *ranks, int64_t n_adapters, int64_t r_max,

@@ -123,7 +123,7 @@ lib.cq_timing_read_launches.argtypes = [_P, _P, _I64, ctypes.POINTER(_I64)]
 lib.cq_timing_read_launches.restype = ctypes.c_int
 lib.cq_residual_norm.argtypes = [_P, _I64] + [_P] * 12
 lib.cq_residual_norm.restype = ctypes.c_int
-lib.cq_lora_add_workspace_size.argtypes = [_I64, _I64]
+lib.cq_lora_add_workspace_size.argtypes = [_I64, _I64, _I64]
 lib.cq_lora_add_workspace_size.restype = _SZ
 lib.cq_lora_add.argtypes = [_P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _I64,
                             _I64, _P, _SZ, _P]
@@ -413,8 +413,8 @@ def cq_residual_norm(resid: torch.Tensor, y=None, *, norm: str = "rms", eps: flo
                                resid_out, x_out, q_out, s_out, stream)
 
 
-def cq_lora_add_workspace_size(M: int, n_adapters: int) -> int:
-    return int(lib.cq_lora_add_workspace_size(M, n_adapters))
+def cq_lora_add_workspace_size(M: int, n_adapters: int, r_max: int) -> int:
+    return int(lib.cq_lora_add_workspace_size(M, n_adapters, r_max))
 
 
 def cq_lora_add(x: torch.Tensor, ids: torch.Tensor, a: torch.Tensor, b: torch.Tensor,

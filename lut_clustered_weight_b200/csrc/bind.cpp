@@ -262,7 +262,7 @@ PyObject *lora_add(PyObject *const *a) {
 
     OnStream on(a[9], c.dev);
     Tensor ws;
-    size_t bytes = cq_lora_add_workspace_size(M, n);
+    size_t bytes = cq_lora_add_workspace_size(M, n, r);
     void *p_w = nullptr;
     if (a[8] != Py_None) {
         const Tensor &w = c.tensor(a[8], "workspace");

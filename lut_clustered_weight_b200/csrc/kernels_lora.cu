@@ -57,6 +57,9 @@ struct LoraArgs {
     const int *n_tiles;
     const LoraTile *tiles;
     const int *perm;
+    __half *t;        // [2][M][R]: hi, lo of the sorted rows
+    float *factor;    // [M]
+    int splits;       // CTAs a tile's columns are shared out to (k_lora_out)
 };
 
 CQ_DEV int valid_id(int id, int n) { return (unsigned)id < (unsigned)n ? id : -1; }
@@ -130,12 +133,14 @@ struct LoraShape {
     static constexpr int pitch = 2 * KC + 16;             // bytes of a staged row (ldmatrix: no conflicts)
     static constexpr int rows = TM + R;                   // x rows, then A rows
     static constexpr int stage = rows * pitch;
-    static constexpr int t_bytes = 2 * TM * (R + 8) * 2;  // hi, lo
+    // halves a row of hi / lo: 8 rows of a fragment load hit different banks (16-byte
+    // loads: rows 64 bytes apart modulo 128; R 16, 8-byte loads: 32)
+    static constexpr int LDT = R <= 32 ? R : R + 32;
+    static constexpr int t_bytes = 2 * TM * LDT * 2;      // hi, lo
     static constexpr int fit = (110 * 1024 - t_bytes) / stage;   // two CTAs an SM
-    static constexpr int NS = fit > 6 ? 6 : fit < 2 ? 2 : fit;   // stages
+    static constexpr int NS = fit > 4 ? 4 : fit < 2 ? 2 : fit;   // stages
     static constexpr int WK = TM == 16 ? kLoraWarps : 1;  // partial t of a CTA (warps along k)
     static constexpr int LDP = R + 8;                     // floats a row of the partial t
-    static constexpr int LDT = R + 8;                     // halves a row of hi / lo
     static constexpr int part_bytes = WK * TM * LDP * 4;
     static constexpr int pool = NS * stage > part_bytes ? NS * stage : part_bytes;
     static constexpr size_t smem = (size_t)pool + t_bytes;
@@ -195,7 +200,8 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
     // ldmatrix rows of this lane: x rows, and n rows (two n8 tiles at once)
     const uint32_t ring0 = smem_u32(ring);
     const uint32_t xa = (16 * wm + (lane & 15)) * S::pitch + 16 * (lane >> 4);
-    const uint32_t wa = (TM + 8 * NT * wn + (lane & 7) + 8 * (lane >> 4)) * S::pitch +
+    // (a warp with one n8 tile reads it twice)
+    const uint32_t wa = (TM + 8 * NT * wn + (lane & 7) + (NT > 1 ? 8 * (lane >> 4) : 0)) * S::pitch +
                         16 * ((lane >> 3) & 1);
 #pragma unroll
     for (int i = 0; i < S::NS - 1; i++) {
@@ -222,8 +228,6 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
 #pragma unroll
                 for (int j = 0; j < NT; j += 2) {
                     uint32_t b[4];
-                    // (a single n8 tile: the second half of the lanes reads rows beyond it,
-                    // inside the stage or the next one, and its result is not used)
                     ldmatrix4(b, base + wa + j * 8 * S::pitch + kb);
                     mma_16816(acc[j], a, b[0], b[1]);
                     if (j + 1 < NT) mma_16816(acc[j + 1], a, b[2], b[3]);
@@ -254,13 +258,40 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
     }
 }
 
+// A warp's row of t as hi + lo in units of a power of two, and that unit times the
+// adapter's scale.
+template <int R>
+CQ_DEV void split_row(const float (&v)[(R + 31) / 32], float sc, __half *hi, __half *lo,
+                      float *factor) {
+    constexpr int PER = (R + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; i++) mx = fmaxf(mx, fabsf(v[i]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 2^-e and 2^e of the largest entry's exponent, both normal numbers
+    const int e = min(max((__float_as_int(mx) >> 23) & 255, 1), 253);
+    const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const float t = v[i] * down;
+        const __half h = __float2half_rn(t);
+        if (R >= 32 || lane < R) {
+            hi[lane + 32 * i] = h;
+            lo[lane + 32 * i] = __float2half_rn(t - __half2float(h));
+        }
+    }
+    if (lane == 0) *factor = sc * up;
+}
+
 // t of the whole cluster, a warp per row, as hi + lo and the factor of the row.
 template <int TM, int R>
 CQ_DEV void gather_t(cg::cluster_group &cluster, float *part, int C, int rows, float sc, __half *th,
                      __half *tl, float *s_factor) {
     using S = LoraShape<TM, R>;
     constexpr int PER = (R + 31) / 32;
-    constexpr int RB = TM == 16 || PER > 2 ? 2 : 4;  // rows a warp has in flight
+    constexpr int RB = TM == 16 ? 2 : PER > 2 ? 4 : 8;  // rows a warp has in flight
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
     for (int r0 = warp; r0 < TM; r0 += RB * kLoraWarps) {
@@ -294,41 +325,49 @@ CQ_DEV void gather_t(cg::cluster_group &cluster, float *part, int C, int rows, f
 #pragma unroll
         for (int b = 0; b < RB; b++) {
             const int row = r0 + b * kLoraWarps;
-            float mx = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER; i++) mx = fmaxf(mx, fabsf(v[b][i]));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // 2^-e and 2^e of the largest entry's exponent, both normal numbers
-            const int e = min(max((__float_as_int(mx) >> 23) & 255, 1), 253);
-            const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
-#pragma unroll
-            for (int i = 0; i < PER; i++) {
-                const float t = v[b][i] * down;
-                const __half hi = __float2half_rn(t);
-                if (R >= 32 || lane < R) {
-                    th[row * S::LDT + lane + 32 * i] = hi;
-                    tl[row * S::LDT + lane + 32 * i] = __float2half_rn(t - __half2float(hi));
-                }
-            }
-            if (lane == 0) s_factor[row] = sc * up;
+            split_row<R>(v[b], sc, th + row * S::LDT, tl + row * S::LDT, s_factor + row);
         }
     }
 }
 
-// Expansion of a block of 8 NB columns: MMA column 2q + e of n8 tile j is column
+// Expansion.  A warp has 16 rows of the tile, whose t it keeps in fragments, and
+// goes over column blocks of 8 NB: MMA column 2q + e of n8 tile j is column
 // 2 NB q + 2j + e of the block, so a lane holds 2 NB consecutive columns of y.
 template <int R, int NB>
 struct Expand {
     static constexpr int KS = R >= 32 ? R / 32 : 1;   // 32-wide steps of the rank
     static constexpr int W = 8 * NB;                  // columns
-    static constexpr int LDT = R + 8;
+    struct T {
+        uint4 a[2][KS], b[2][KS];  // rows g and g + 8 of lo, hi
+    };
+    // (hi0, lo0: row g; hi1, lo1: row g + 8)
+    CQ_DEV static void load_t(T &o, const __half *hi0, const __half *lo0, const __half *hi1,
+                              const __half *lo1) {
+        const int q = threadIdx.x & 3;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const __half *ta = h ? hi0 : lo0, *tb = h ? hi1 : lo1;
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                if (R >= 32) {
+                    o.a[h][s] = *reinterpret_cast<const uint4 *>(ta + 32 * s + 8 * q);
+                    o.b[h][s] = *reinterpret_cast<const uint4 *>(tb + 32 * s + 8 * q);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(ta + 4 * q);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(tb + 4 * q);
+                    o.a[h][s] = make_uint4(u.x, u.y, 0, 0);
+                    o.b[h][s] = make_uint4(v.x, v.y, 0, 0);
+                }
+            }
+        }
+    }
     struct B {
         uint4 w[NB][KS];
     };
     struct Y {
         float4 a[NB / 2], b[NB / 2];
     };
+    static constexpr int pieces = NB;  // 16-byte pieces of y a lane has per block and 16 rows
 
     CQ_DEV static void load_b(B &o, const LoraArgs &p, int id, int rank, int n0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -353,6 +392,23 @@ struct Expand {
             }
         }
     }
+    // the same from staged rows; row: the one of n8 tile 0 that this lane reads
+    CQ_DEV static void take_b(B &o, const unsigned char *row, int pitch) {
+        const int q = threadIdx.x & 3;
+#pragma unroll
+        for (int j = 0; j < NB; j++) {
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                const unsigned char *at = row + 2 * j * pitch;
+                if (R >= 32) {
+                    o.w[j][s] = *reinterpret_cast<const uint4 *>(at + 64 * s + 16 * q);
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(at + 8 * q);
+                    o.w[j][s] = make_uint4(v.x, v.y, 0, 0);
+                }
+            }
+        }
+    }
     // what lies beyond the rank in a chunk that holds its end is not used
     CQ_DEV static void cut_b(B &o, int rank) {
         const int q = threadIdx.x & 3;
@@ -362,64 +418,59 @@ struct Expand {
             for (int s = 0; s < KS; s++)
                 o.w[j][s] = keep_first(o.w[j][s], rank - (R >= 32 ? 32 * s + 8 * q : 4 * q));
     }
-    CQ_DEV static void load_y(Y &o, const LoraArgs &p, const int *s_rows, int ra, int rows, int n0) {
-        const int q = threadIdx.x & 3, c = n0 + 2 * NB * q, rb = ra + 8;
-        const float *pa = p.y + (int64_t)s_rows[ra] * p.ldy + c;
-        const float *pb = p.y + (int64_t)s_rows[rb] * p.ldy + c;
+    // y of a block and 16 rows into this thread's own pieces of a slot (256
+    // pieces apart), and from there: no other thread reads them, so no barrier
+    // (ya, yb: y at column 2 NB q of the warp's rows g and g + 8, NULL: no row)
+    CQ_DEV static void fetch_y(unsigned char *slot, const float *ya, const float *yb, int N, int n0) {
+        const int c = n0 + 2 * NB * (threadIdx.x & 3);
+        unsigned char *dst = slot + 16 * threadIdx.x;
 #pragma unroll
         for (int i = 0; i < NB / 2; i++) {
-            const bool in = c + 4 * i < p.N;  // N % 8 == 0
-            o.a[i] = in && ra < rows ? reinterpret_cast<const float4 *>(pa)[i] : make_float4(0, 0, 0, 0);
-            o.b[i] = in && rb < rows ? reinterpret_cast<const float4 *>(pb)[i] : make_float4(0, 0, 0, 0);
+            const bool in = c + 4 * i < N;  // N % 8 == 0
+            if (in && ya) cp_async16_zfill(dst + 2 * i * 16 * kLoraThreads, ya + n0 + 4 * i, 16);
+            if (in && yb) cp_async16_zfill(dst + (2 * i + 1) * 16 * kLoraThreads, yb + n0 + 4 * i, 16);
         }
     }
-    CQ_DEV static void run(const B &w, const Y &y, const LoraArgs &p, const int *s_rows,
-                           const float *s_factor, const __half *th, const __half *tl, int ra,
-                           int rows, int n0) {
-        const int q = threadIdx.x & 3, rb = ra + 8, c = n0 + 2 * NB * q;
+    CQ_DEV static void take_y(Y &o, const unsigned char *slot) {
+        const float4 *src = reinterpret_cast<const float4 *>(slot) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < NB / 2; i++) {
+            o.a[i] = src[2 * i * kLoraThreads];
+            o.b[i] = src[(2 * i + 1) * kLoraThreads];
+        }
+    }
+    CQ_DEV static void run(const B &w, const T &t, const Y &y, float fa, float fb, float *oa,
+                           float *ob, int N, int n0) {
+        const int c = n0 + 2 * NB * (threadIdx.x & 3);
         float acc[NB][4];
 #pragma unroll
         for (int j = 0; j < NB; j++)
 #pragma unroll
             for (int e = 0; e < 4; e++) acc[j][e] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < KS; s++) {
+        for (int h = 0; h < 2; h++) {  // lo first, then hi
 #pragma unroll
-            for (int part_i = 0; part_i < 2; part_i++) {  // lo first, then hi
-                const __half *tp = part_i ? th : tl;
-                if (R >= 32) {
-                    const uint4 va = *reinterpret_cast<const uint4 *>(tp + ra * LDT + 32 * s + 8 * q);
-                    const uint4 vb = *reinterpret_cast<const uint4 *>(tp + rb * LDT + 32 * s + 8 * q);
+            for (int s = 0; s < KS; s++) {
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const uint32_t a[4] = {word(va, 2 * h), word(vb, 2 * h), word(va, 2 * h + 1),
-                                               word(vb, 2 * h + 1)};
+                for (int m = 0; m < (R >= 32 ? 2 : 1); m++) {
+                    const uint32_t a[4] = {word(t.a[h][s], 2 * m), word(t.b[h][s], 2 * m),
+                                           word(t.a[h][s], 2 * m + 1), word(t.b[h][s], 2 * m + 1)};
 #pragma unroll
-                        for (int j = 0; j < NB; j++)
-                            mma_16816(acc[j], a, word(w.w[j][s], 2 * h), word(w.w[j][s], 2 * h + 1));
-                    }
-                } else {
-                    const uint2 va = *reinterpret_cast<const uint2 *>(tp + ra * LDT + 4 * q);
-                    const uint2 vb = *reinterpret_cast<const uint2 *>(tp + rb * LDT + 4 * q);
-                    const uint32_t a[4] = {va.x, vb.x, va.y, vb.y};
-#pragma unroll
-                    for (int j = 0; j < NB; j++) mma_16816(acc[j], a, w.w[j][s].x, w.w[j][s].y);
+                    for (int j = 0; j < NB; j++)
+                        mma_16816(acc[j], a, word(w.w[j][s], 2 * m), word(w.w[j][s], 2 * m + 1));
                 }
             }
         }
-        const float fa = s_factor[ra], fb = s_factor[rb];
-        float *oa = p.out + (int64_t)s_rows[ra] * p.ldo + c;
-        float *ob = p.out + (int64_t)s_rows[rb] * p.ldo + c;
 #pragma unroll
         for (int i = 0; i < NB / 2; i++) {
             const float(&l)[4] = acc[2 * i], (&h)[4] = acc[2 * i + 1];
-            if (c + 4 * i < p.N) {
-                if (ra < rows)
-                    reinterpret_cast<float4 *>(oa)[i] =
+            if (c + 4 * i < N) {
+                if (oa)
+                    reinterpret_cast<float4 *>(oa + n0)[i] =
                         make_float4(y.a[i].x + fa * l[0], y.a[i].y + fa * l[1], y.a[i].z + fa * h[0],
                                     y.a[i].w + fa * h[1]);
-                if (rb < rows)
-                    reinterpret_cast<float4 *>(ob)[i] =
+                if (ob)
+                    reinterpret_cast<float4 *>(ob + n0)[i] =
                         make_float4(y.b[i].x + fb * l[2], y.b[i].y + fb * l[3], y.b[i].z + fb * h[2],
                                     y.b[i].w + fb * h[3]);
             }
@@ -427,6 +478,19 @@ struct Expand {
     }
 };
 
+// out = y for the columns [c0, c1) of a tile without an adapter.
+CQ_DEV void copy_rows(const LoraArgs &p, const int *s_rows, int rows, int c0, int c1) {
+    if (p.y == p.out) return;
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < rows; i += kLoraWarps) {
+        const float *src = p.y + (int64_t)s_rows[i] * p.ldy;
+        float *dst = p.out + (int64_t)s_rows[i] * p.ldo;
+        for (int c = c0 + 4 * lane; c < c1; c += 128)
+            *reinterpret_cast<float4 *>(dst + c) = *reinterpret_cast<const float4 *>(src + c);
+    }
+}
+
+// ---------------------------------------------------------------- few rows: one launch
 template <int TM, int R>
 __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     using S = LoraShape<TM, R>;
@@ -448,19 +512,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     griddep_launch();
 
     // ---- the tile: adapter and rows (the same for every CTA of the cluster)
-    if (p.tiles) {
-        if (tile >= *p.n_tiles) return;
-        const LoraTile T = p.tiles[tile];
-        for (int i = threadIdx.x; i < TM; i += kLoraThreads)
-            s_rows[i] = p.perm[T.start + min(i, T.rows - 1)];
-        if (threadIdx.x == 0) {
-            s_id = T.id;
-            s_count = T.rows;
-        }
-        __syncthreads();
-    } else if (!find_tile(p, tile, TM, reinterpret_cast<int *>(smem), s_rows, &s_id, &s_count)) {
-        return;
-    }
+    if (!find_tile(p, tile, TM, reinterpret_cast<int *>(smem), s_rows, &s_id, &s_count)) return;
     const int id = s_id, rows = s_count;
     const int rank = id < 0 ? 0 : p.ranks ? max(0, min(p.ranks[id], p.r)) : p.r;
     const float sc = id >= 0 && p.scale ? p.scale[id] : 1.0f;
@@ -469,15 +521,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     const int nblk = (p.N + X::W - 1) / X::W;
     const int nb0 = (int)((int64_t)crank * nblk / C), nb1 = (int)((int64_t)(crank + 1) * nblk / C);
     const int c0 = nb0 * X::W, c1 = min(nb1 * X::W, p.N);
-    if (rank == 0) {  // out = y
-        if (p.y != p.out) {
-            for (int i = warp; i < rows; i += kLoraWarps) {
-                const float *src = p.y + (int64_t)s_rows[i] * p.ldy;
-                float *dst = p.out + (int64_t)s_rows[i] * p.ldo;
-                for (int c = c0 + 4 * lane; c < c1; c += 128)
-                    *reinterpret_cast<float4 *>(dst + c) = *reinterpret_cast<const float4 *>(src + c);
-            }
-        }
+    if (rank == 0) {
+        copy_rows(p, s_rows, rows, c0, c1);
         return;
     }
     // B's part for the expansion, into the L2 while the shrink runs
@@ -491,39 +536,221 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
         shrink<TM, R>(p, id, rows, rank, s_rows, smem, part, (int)((int64_t)crank * chunks / C),
                       (int)((int64_t)(crank + 1) * chunks / C));
     }
-    // the first block's operands do not wait for t
-    int nb = nb0 + warp;
+    // ---- expand.  y comes by cp.async, D blocks ahead, into slots behind the partial
+    // t (which the other CTAs still read); the next block's B is requested a block
+    // ahead
+    constexpr int y_off = TM * S::LDP * 4, slot_bytes = X::pieces * 16 * kLoraThreads;
+    constexpr int room = (S::pool - y_off) / slot_bytes;
+    constexpr int D = room > 8 ? 8 : room;
+    static_assert(D >= 1, "no room for y");
+    constexpr int MB = TM / 16, WC = kLoraWarps / MB;  // warps along the rows, along the columns
+    unsigned char *slots = smem + y_off;
+    const int ra = 16 * (warp % MB) + g, rb = ra + 8, cq = 2 * NB * (lane & 3);
+    const bool busy = 16 * (warp % MB) < rows;
+    const float *ya = ra < rows ? p.y + (int64_t)s_rows[ra] * p.ldy + cq : nullptr;
+    const float *yb = rb < rows ? p.y + (int64_t)s_rows[rb] * p.ldy + cq : nullptr;
+    float *oa = ra < rows ? p.out + (int64_t)s_rows[ra] * p.ldo + cq : nullptr;
+    float *ob = rb < rows ? p.out + (int64_t)s_rows[rb] * p.ldo + cq : nullptr;
+    int nb = busy ? nb0 + warp / MB : nb1;  // block of this step
+    int fn = nb, fs = 0;                    // block and slot of the next request
+    auto request = [&]() {
+        if (fn < nb1) X::fetch_y(slots + fs * slot_bytes, ya, yb, p.N, fn * X::W);
+        fn += WC;
+        cp_async_commit_group();
+        fs = fs + 1 == D ? 0 : fs + 1;
+    };
+    if (S::WK > 1) __syncthreads();  // the warps' sums are read
+#pragma unroll 1
+    for (int i = 0; i < D; i++) request();
     typename X::B w, wn;
-    typename X::Y y, yn;
-    if (nb < nb1) {
-        X::load_b(w, p, id, rank, nb * X::W);
-        X::load_y(y, p, s_rows, g, rows, nb * X::W);
-    }
+    if (nb < nb1) X::load_b(w, p, id, rank, nb * X::W);
     cluster.sync();
     gather_t<TM, R>(cluster, part, C, rows, sc, th, tl, s_factor);
     __syncthreads();
     cluster.barrier_arrive();  // this CTA has read every partial t
 
-    // ---- expand: a warp per column block, over the tile's rows 16 at a time, the
-    // next y (and B) requested before this block's products
-    const int mbs = (rows + 15) >> 4;
-    for (; nb < nb1; nb += kLoraWarps) {
-        const int nn = nb + kLoraWarps;
-        const bool more = nn < nb1;
-        if (more) X::load_b(wn, p, id, rank, nn * X::W);
+    typename X::T t;
+    X::load_t(t, th + ra * S::LDT, tl + ra * S::LDT, th + rb * S::LDT, tl + rb * S::LDT);
+    const float fa = s_factor[ra], fb = s_factor[rb];
+    int slot = 0;
+    for (; nb < nb1; nb += WC) {
+        if (nb + WC < nb1) X::load_b(wn, p, id, rank, (nb + WC) * X::W);
         X::cut_b(w, rank);
-        for (int mb = 0; mb < mbs; mb++) {
-            if (mb + 1 < mbs)
-                X::load_y(yn, p, s_rows, 16 * (mb + 1) + g, rows, nb * X::W);
-            else if (more)
-                X::load_y(yn, p, s_rows, g, rows, nn * X::W);
-            X::run(w, y, p, s_rows, s_factor, th, tl, 16 * mb + g, rows, nb * X::W);
-            y = yn;
-        }
+        typename X::Y y;
+        cp_async_wait_group<D - 1>();
+        X::take_y(y, slots + slot * slot_bytes);
+        X::run(w, t, y, fa, fb, oa, ob, p.N, nb * X::W);
+        request();  // into the slot just taken
+        slot = slot + 1 == D ? 0 : slot + 1;
         w = wn;
     }
+    cp_async_wait_group<0>();
     __syncwarp();
     cluster.barrier_wait();  // no CTA leaves while another may read its partial t
+}
+
+// ---------------------------------------------------------------- many rows
+// Above kLoraSmallM rows the two products are launches of their own: a tile's
+// shrink is short and waits on latencies, its expansion streams y, and in one
+// launch all CTAs would be in the same phase at the same time (4096 rows, K 2048,
+// N 2816, rank 64: 20 of 45 us with y on its way).
+template <int TM>
+CQ_DEV bool planned_tile(const LoraArgs &p, int tile, int *s_rows, LoraTile &T) {
+    if (tile >= __ldcg(p.n_tiles)) return false;
+    const int4 v = __ldcg(reinterpret_cast<const int4 *>(p.tiles + tile));
+    T = LoraTile{v.x, v.y, v.z, v.w};
+    if (threadIdx.x < TM)
+        s_rows[threadIdx.x] = __ldcg(p.perm + T.start + min((int)threadIdx.x, T.rows - 1));
+    __syncthreads();
+    return true;
+}
+CQ_DEV int rank_of(const LoraArgs &p, int id) {
+    return id < 0 ? 0 : p.ranks ? max(0, min(__ldcg(p.ranks + id), p.r)) : p.r;
+}
+
+// t = A x of a tile by a cluster: the CTAs split K, then each sums the partial t of
+// its share of the rows over the cluster and stores them as hi, lo and factor.
+template <int TM, int R>
+__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_t(const LoraArgs p) {
+    using S = LoraShape<TM, R>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *part = reinterpret_cast<float *>(smem);
+    __shared__ int s_rows[TM];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
+    griddep_wait();
+    griddep_launch();
+    LoraTile T;
+    if (!planned_tile<TM>(p, blockIdx.x / C, s_rows, T)) return;
+    const int rank = rank_of(p, T.id);
+    if (rank == 0) return;
+    const float sc = p.scale ? p.scale[T.id] : 1.0f;
+    const int chunks = (p.K + S::KC - 1) / S::KC;
+    shrink<TM, R>(p, T.id, T.rows, rank, s_rows, smem, part, (int)((int64_t)crank * chunks / C),
+                  (int)((int64_t)(crank + 1) * chunks / C));
+    cluster.sync();
+    constexpr int PER = (R + 31) / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int row = crank * kLoraWarps + warp; row < T.rows; row += C * kLoraWarps) {
+        float v[PER];
+#pragma unroll
+        for (int i = 0; i < PER; i++) v[i] = 0.0f;
+        for (int c = 0; c < C; c += 4) {  // C is a multiple of 4
+            float u[4][PER];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float *rp = cluster.map_shared_rank(part, c + k) + row * S::LDP;
+#pragma unroll
+                for (int i = 0; i < PER; i++)
+                    u[k][i] = R >= 32 || lane < R ? rp[lane + 32 * i] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+#pragma unroll
+                for (int i = 0; i < PER; i++) v[i] += u[k][i];
+        }
+        const int64_t at = T.start + row;
+        split_row<R>(v, sc, p.t + at * R, p.t + ((int64_t)p.M + at) * R, p.factor + at);
+    }
+    cluster.sync();  // no CTA leaves while another may read its partial t
+}
+
+// out = y + factor * B t of a tile's share of the columns.  A warp has 16 rows of the
+// tile and a share of the columns of each step; a ring of stages holds a step's rows
+// of B (shared by the warps of the same columns) and its y (every thread its own).
+// Nothing before k_lora_t can still be running when this kernel starts (k_lora_t lets it
+// start after its own wait), so the tile, y and B are requested before the wait for
+// t; the tile past the L1, which may hold an earlier call's.
+template <int TM, int R>
+struct OutShape {
+    static constexpr int NB = 2;                           // n8 tiles of a warp's step
+    static constexpr int MB = TM / 16, WC = kLoraWarps / MB;  // warps along the rows, along the columns
+    static constexpr int W = WC * 8 * NB;                  // columns of a step
+    // bytes of a staged row of B: the 8 rows of a fragment load hit different banks
+    static constexpr int pitch = R >= 64 ? 2 * R + 64 : 2 * R;
+    static constexpr int y_off = W * pitch;
+    static constexpr int stage = y_off + NB * 16 * kLoraThreads;
+    static constexpr int fit = 100 * 1024 / stage;         // two CTAs an SM
+    static constexpr int D = fit > 8 ? 8 : fit < 2 ? 2 : fit;
+};
+
+template <int TM, int R>
+__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) {
+    using S = OutShape<TM, R>;
+    using X = Expand<R, S::NB>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int s_rows[TM];
+    const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    LoraTile T;
+    if (!planned_tile<TM>(p, tile, s_rows, T)) {
+        griddep_wait();  // this kernel ends after k_lora_t, whatever its CTAs had to do
+        return;
+    }
+    const int rows = T.rows, rank = rank_of(p, T.id);
+    const int nblk = (p.N + S::W - 1) / S::W;
+    const int nb0 = (int)((int64_t)split * nblk / p.splits);
+    const int nb1 = (int)((int64_t)(split + 1) * nblk / p.splits);
+    if (rank == 0) {
+        griddep_wait();
+        copy_rows(p, s_rows, rows, nb0 * S::W, min(nb1 * S::W, p.N));
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int ra = 16 * (warp % S::MB) + g, rb = ra + 8, wc = warp / S::MB;
+    const int cw = wc * X::W;                   // the warp's columns in a step
+    const bool busy = 16 * (warp % S::MB) < rows;
+    const int cq = 2 * S::NB * q;
+    const float *ya = ra < rows ? p.y + (int64_t)s_rows[ra] * p.ldy + cq : nullptr;
+    const float *yb = rb < rows ? p.y + (int64_t)s_rows[rb] * p.ldy + cq : nullptr;
+    float *oa = ra < rows ? p.out + (int64_t)s_rows[ra] * p.ldo + cq : nullptr;
+    float *ob = rb < rows ? p.out + (int64_t)s_rows[rb] * p.ldo + cq : nullptr;
+    // 16-byte pieces of a step's rows of B: PR a row, up to r (zeros beyond the rank's
+    // last piece)
+    constexpr int PR = R / 8, PB = S::W * PR, PASSES = (PB + kLoraThreads - 1) / kLoraThreads;
+    const __half *bbase = p.b + (int64_t)T.id * p.N * p.r;
+    auto request = [&](int nb, int slot) {
+        unsigned char *st = smem + slot * S::stage;
+        if (nb < nb1) {
+#pragma unroll
+            for (int i = 0; i < PASSES; i++) {
+                const int pc = tid + i * kLoraThreads;
+                if (PB % kLoraThreads == 0 || pc < PB) {
+                    const int row = pc / PR, k = 8 * (pc % PR), col = min(nb * S::W + row, p.N - 1);
+                    const bool in = k < rank;
+                    cp_async16_zfill(st + row * S::pitch + 2 * k,
+                                     in ? bbase + (int64_t)col * p.r + k : p.b, in ? 16 : 0);
+                }
+            }
+            X::fetch_y(st + S::y_off, ya, yb, p.N, nb * S::W + cw);
+        }
+        cp_async_commit_group();
+    };
+    int slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < S::D - 1; i++) request(nb0 + i, i);
+    griddep_wait();
+    griddep_launch();
+    typename X::T t;
+    const int64_t a0 = T.start + min(ra, rows - 1), b0 = T.start + min(rb, rows - 1);
+    const __half *lo = p.t + (int64_t)p.M * R;
+    X::load_t(t, p.t + a0 * R, lo + a0 * R, p.t + b0 * R, lo + b0 * R);
+    const float fa = p.factor[a0], fb = p.factor[b0];
+    for (int nb = nb0; nb < nb1; nb++) {
+        cp_async_wait_group<S::D - 2>();
+        __syncthreads();  // every thread's pieces are here; the slot taken last is free
+        request(nb + S::D - 1, slot == 0 ? S::D - 1 : slot - 1);
+        if (busy) {
+            const unsigned char *st = smem + slot * S::stage;
+            typename X::B w;
+            X::take_b(w, st + (cw + 4 * (g >> 1) + (g & 1)) * S::pitch, S::pitch);
+            X::cut_b(w, rank);
+            typename X::Y y;
+            X::take_y(y, st + S::y_off);
+            X::run(w, t, y, fa, fb, oa, ob, p.N, nb * S::W + cw);
+        }
+        slot = slot + 1 == S::D ? 0 : slot + 1;
+    }
+    cp_async_wait_group<0>();
 }
 
 // ---------------------------------------------------------------- rows by adapter
@@ -642,39 +869,58 @@ static int lora_tile_rows(int64_t M) { return M >= 2048 ? 64 : 16; }
 static int64_t lora_max_tiles(int64_t M, int64_t n) {
     return M / lora_tile_rows(M) + std::min(n + 1, M);
 }
-// Scratch of a planned call: tile count, tile list, permutation, places.
+static int lora_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+// Scratch of a planned call: tile count, tile list, permutation, places, t, factors.
 struct LoraScratch {
-    size_t tiles, perm, place, total;
+    size_t tiles, perm, place, t, factor, total;
 };
-static LoraScratch lora_scratch(int64_t M, int64_t n) {
+static LoraScratch lora_scratch(int64_t M, int64_t n, int64_t r) {
     LoraScratch s{};
     s.tiles = 256;
     s.perm = s.tiles + align256(lora_max_tiles(M, n) * sizeof(LoraTile));
     s.place = s.perm + align256(M * sizeof(int));
-    s.total = s.place + (M > kPlanRows * kPlanThreads ? align256(M * sizeof(int)) : 0);
+    s.t = s.place + (M > kPlanRows * kPlanThreads ? align256(M * sizeof(int)) : 0);
+    s.factor = s.t + align256(2 * M * lora_rank(r) * sizeof(__half));
+    s.total = s.factor + align256(M * sizeof(float));
     return s;
 }
 
-template <int TM, int R>
-static cudaError_t launch_tiles(const LoraArgs &p, int64_t tiles, int C, cudaStream_t st) {
+// One cluster per tile: 8 CTAs, or 4 where a tile's A and B are small (12 KB: 6.5 us
+// with 4, 7.3 with 8; 280 KB: 8.4 and 6.8).
+template <int R>
+static cudaError_t launch_small(const LoraArgs &p, cudaStream_t st) {
+    const int C = ((int64_t)p.K + p.N) * p.r * 2 < 96 * 1024 ? 4 : 8;
     count_launch();
-    return launch_pdl(k_lora<TM, R>, dim3((unsigned)(tiles * C)), dim3(kLoraThreads),
-                      LoraShape<TM, R>::smem, st, C, p);
+    return launch_pdl(k_lora<16, R>, dim3((unsigned)(lora_max_tiles(p.M, p.n) * C)),
+                      dim3(kLoraThreads), LoraShape<16, R>::smem, st, C, p);
 }
 
-template <int TM>
-static cudaError_t launch_rank(const LoraArgs &p, int64_t tiles, int C, cudaStream_t st) {
-    if (p.r <= 16) return launch_tiles<TM, 16>(p, tiles, C, st);
-    if (p.r <= 32) return launch_tiles<TM, 32>(p, tiles, C, st);
-    if (p.r <= 64) return launch_tiles<TM, 64>(p, tiles, C, st);
-    return launch_tiles<TM, 128>(p, tiles, C, st);
+template <int TM, int R>
+static cudaError_t launch_planned(LoraArgs p, cudaStream_t st) {
+    constexpr int C = TM == 16 ? 8 : 4;
+    const int64_t tiles = lora_max_tiles(p.M, p.n);
+    count_launch(2);
+    cudaError_t e = launch_pdl(k_lora_t<TM, R>, dim3((unsigned)(tiles * C)), dim3(kLoraThreads),
+                               (size_t)LoraShape<TM, R>::pool, st, C, p);
+    if (e != cudaSuccess) return e;
+    // column shares of a tile: two CTAs an SM in all, of at least four steps each
+    using S = OutShape<TM, R>;
+    const int nblk = (p.N + S::W - 1) / S::W;
+    const int64_t full = std::max<int64_t>(1, p.M / TM);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(2LL * sm_count() / full, nblk / 4));
+    return launch_pdl(k_lora_out<TM, R>, dim3((unsigned)(tiles * p.splits)), dim3(kLoraThreads),
+                      (size_t)S::D * S::stage, st, 1, p);
 }
 
 static cudaError_t launch_lora(LoraArgs p, void *ws, cudaStream_t st) {
     TimedScope ts(st, CQ_KERNEL_LORA_ADD);
-    const int64_t tiles = lora_max_tiles(p.M, p.n);
-    if (p.M <= kLoraSmallM) return launch_rank<16>(p, tiles, 8, st);
-    const LoraScratch s = lora_scratch(p.M, p.n);
+    const int R = lora_rank(p.r);
+    if (p.M <= kLoraSmallM)
+        return R == 16   ? launch_small<16>(p, st)
+               : R == 32 ? launch_small<32>(p, st)
+               : R == 64 ? launch_small<64>(p, st)
+                         : launch_small<128>(p, st);
+    const LoraScratch s = lora_scratch(p.M, p.n, p.r);
     uint8_t *w = reinterpret_cast<uint8_t *>(ws);
     int *n_tiles = reinterpret_cast<int *>(w);
     LoraTile *list = reinterpret_cast<LoraTile *>(w + s.tiles);
@@ -688,18 +934,29 @@ static cudaError_t launch_lora(LoraArgs p, void *ws, cudaStream_t st) {
     p.n_tiles = n_tiles;
     p.tiles = list;
     p.perm = perm;
-    return TM == 16 ? launch_rank<16>(p, tiles, 8, st) : launch_rank<64>(p, tiles, 4, st);
+    p.t = reinterpret_cast<__half *>(w + s.t);
+    p.factor = reinterpret_cast<float *>(w + s.factor);
+    if (TM == 16)
+        return R == 16   ? launch_planned<16, 16>(p, st)
+               : R == 32 ? launch_planned<16, 32>(p, st)
+               : R == 64 ? launch_planned<16, 64>(p, st)
+                         : launch_planned<16, 128>(p, st);
+    return R == 16   ? launch_planned<64, 16>(p, st)
+           : R == 32 ? launch_planned<64, 32>(p, st)
+           : R == 64 ? launch_planned<64, 64>(p, st)
+                     : launch_planned<64, 128>(p, st);
 }
 
 }  // namespace cq
 
 extern "C" {
 
-CQ_API size_t cq_lora_add_workspace_size(int64_t M, int64_t n_adapters) {
+CQ_API size_t cq_lora_add_workspace_size(int64_t M, int64_t n_adapters, int64_t r_max) {
     using namespace cq;
-    if (M <= kLoraSmallM || M > (int64_t(1) << 24) || n_adapters <= 0 || n_adapters > 4096)
+    if (M <= kLoraSmallM || M > (int64_t(1) << 24) || n_adapters <= 0 || n_adapters > 4096 ||
+        r_max <= 0 || r_max > kLoraMaxRank)
         return 0;
-    return lora_scratch(M, n_adapters).total;
+    return lora_scratch(M, n_adapters, r_max).total;
 }
 
 CQ_API cq_status cq_lora_add(const void *x, const int32_t *ids, int64_t M, int64_t K,
@@ -721,7 +978,7 @@ CQ_API cq_status cq_lora_add(const void *x, const int32_t *ids, int64_t M, int64
         N > (int64_t(1) << 20))
         return CQ_ERR_UNSUPPORTED;
     if (M == 0) return CQ_OK;
-    const size_t need = cq_lora_add_workspace_size(M, n_adapters);
+    const size_t need = cq_lora_add_workspace_size(M, n_adapters, r_max);
     if (need > 0 && (!workspace || workspace_bytes < need)) return CQ_ERR_WORKSPACE;
     LoraArgs p{};
     p.x = reinterpret_cast<const __half *>(x);

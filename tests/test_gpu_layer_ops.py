@@ -246,6 +246,16 @@ LORA_CASES = [
     (256, 64, 40, 300, 16, "rows", False),         # one row a thread of the tile search
     (255, 40, 24, 2, 24, "none", False),
     (2048, 96, 72, 2, 16, "none", True),
+    (2048, 4096, 24, 2, 16, "runs", False),        # every stage of the ring in use, per rank size
+    (2050, 4096, 24, 2, 32, "runs", False),
+    (2048, 4096, 136, 2, 64, "runs", True),
+    (2049, 4096, 40, 2, 128, "runs", True),
+    (300, 8192, 24, 2, 8, "runs", False),
+    (300, 8192, 24, 2, 32, "runs", False),
+    (300, 8192, 24, 2, 64, "runs", False),
+    (300, 8192, 2056, 2, 128, "runs", False),
+    (5, 8192, 4104, 2, 16, "rows", False),
+    (5, 8192, 4104, 2, 128, "rows", False),
     (9000, 16, 24, 5, 8, "rows", False),           # more rows than the sorting CTA holds
     (17000, 8, 8, 1100, 8, "rows", True),
 ]

@@ -131,12 +131,13 @@ def test_lora_add_argument_checks():
 def test_lora_add_workspace():
     for M in (1, 64, 4096, 1 << 20):
         for n in (1, 64, 4096):
-            need = cq.cq_lora_add_workspace_size(M, n)
+            need = cq.cq_lora_add_workspace_size(M, n, 16)
+            assert need <= cq.cq_lora_add_workspace_size(M, n, 128)
             if need:
                 assert _lora_call(M=M, n=n, ws=None, wsb=0) == WSP
                 assert _lora_call(M=M, n=n, wsb=need - 1) == WSP
-    assert cq.cq_lora_add_workspace_size(0, 4) == 0
-    assert cq.cq_lora_add_workspace_size(-1, 4) == 0
+    assert cq.cq_lora_add_workspace_size(0, 4, 16) == 0
+    assert cq.cq_lora_add_workspace_size(-1, 4, 16) == 0
 
 
 # ---------------------------------------------------------------- cq_rope_qkv
