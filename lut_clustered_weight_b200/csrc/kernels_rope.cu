@@ -37,13 +37,47 @@ CQ_DEV uint32_t pack_half2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// What one lane does in a round: its unit of head h.
+struct RopeUnit {
+    int h, c0, c1;  // head, first channel of the unit's two halves
+    bool live, turned, is_v;
+    float4 a, b;
+};
+
+CQ_DEV void load_unit(RopeUnit &u, const RopeArgs &p, const float *row, int h, int h_end, int lane) {
+    u.h = h;
+    u.live = h < h_end && lane < (p.D >> 3);
+    u.is_v = h >= p.n_q + p.n_kv;
+    u.turned = !u.is_v && lane < (p.rot >> 3);
+    const bool apart = u.turned && !p.interleaved;
+    u.c0 = apart ? 4 * lane : 8 * lane;
+    u.c1 = apart ? (p.rot >> 1) + 4 * lane : u.c0 + 4;
+    u.a = u.b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (u.live) {
+        const float *src = row + h * p.D;
+        u.a = __ldcs(reinterpret_cast<const float4 *>(src + u.c0));
+        u.b = __ldcs(reinterpret_cast<const float4 *>(src + u.c1));
+    }
+}
+
 __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
     __shared__ float2 cs[kRopeMaxDim / 2];
     griddep_wait();
     griddep_launch();
     const int64_t m = blockIdx.x;
-    const int half = p.rot >> 1;
-    if (threadIdx.x < half) {
+    const int heads = p.n_q + 2 * p.n_kv;
+    const int G = 1 << p.log2g, lane = threadIdx.x & (G - 1), groups = kRopeThreads >> p.log2g;
+    const int h_end = min(heads, ((int)blockIdx.y + 1) * p.heads_per_cta);
+    int h0 = blockIdx.y * p.heads_per_cta;
+    const int gh = threadIdx.x >> p.log2g;
+    const float *row = p.qkv + m * heads * p.D;
+    // the first round's values are on their way while the angles are formed, every
+    // other round's while the one before is worked on
+    RopeUnit next;
+    load_unit(next, p, row, h0 + gh, h_end, lane);
+    const int64_t slot = p.slots ? p.slots[m] : m;
+    const bool cached = !p.slots || (slot >= 0 && slot < p.n_slots);
+    if (threadIdx.x < (p.rot >> 1)) {
         // in turns, so that the reduction is a subtraction of the nearest whole one
         const double turns =
             (double)p.positions[m] * (double)p.inv_freq[threadIdx.x] * 0.15915494309189535;
@@ -52,79 +86,61 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
         cs[threadIdx.x] = make_float2(c * p.attn_scale, s * p.attn_scale);
     }
     __syncthreads();
-    const int G = 1 << p.log2g, lane = threadIdx.x & (G - 1);
-    const int groups = kRopeThreads >> p.log2g;
-    const int heads = p.n_q + 2 * p.n_kv;
-    const int h_end = min(heads, ((int)blockIdx.y + 1) * p.heads_per_cta);
-    const int64_t slot = p.slots ? p.slots[m] : m;
-    const bool cached = !p.slots || (slot >= 0 && slot < p.n_slots);
     // every lane of a warp runs the same rounds (the shuffles need all of them)
-    for (int h0 = blockIdx.y * p.heads_per_cta; h0 < h_end; h0 += groups) {
-        const int h = h0 + (threadIdx.x >> p.log2g);
-        const bool live = h < h_end && lane < (p.D >> 3);
-        const bool is_v = h >= p.n_q + p.n_kv;
-        const int rot_units = is_v ? 0 : p.rot >> 3;
-        const bool turned = lane < rot_units;
-        // first channel of the unit's two halves
-        const int c0 = turned && !p.interleaved ? 4 * lane : 8 * lane;
-        const int c1 = turned && !p.interleaved ? half + 4 * lane : c0 + 4;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = 0.0f;
-        if (live) {
-            const float *src = p.qkv + (m * heads + h) * p.D;
-            const float4 a = __ldcs(reinterpret_cast<const float4 *>(src + c0));
-            const float4 b = __ldcs(reinterpret_cast<const float4 *>(src + c1));
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        }
-        const __half *w = is_v ? nullptr : h < p.n_q ? p.qw : p.kw;
+    for (; h0 < h_end; h0 += groups) {
+        const RopeUnit u = next;
+        if (h0 + groups < h_end) load_unit(next, p, row, h0 + groups + gh, h_end, lane);
+        float v[8] = {u.a.x, u.a.y, u.a.z, u.a.w, u.b.x, u.b.y, u.b.z, u.b.w};
+        const __half *w = u.is_v ? nullptr : u.h < p.n_q ? p.qw : p.kw;
         if (p.qw || p.kw) {
             float ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; i++) ss += v[i] * v[i];
             for (int o = G >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (w && live) {
+            if (w && u.live) {
                 const float inv = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-                const uint2 w0 = *reinterpret_cast<const uint2 *>(w + c0);
-                const uint2 w1 = *reinterpret_cast<const uint2 *>(w + c1);
-                const __half2 wh[4] = {
-                    *reinterpret_cast<const __half2 *>(&w0.x), *reinterpret_cast<const __half2 *>(&w0.y),
-                    *reinterpret_cast<const __half2 *>(&w1.x), *reinterpret_cast<const __half2 *>(&w1.y)};
+                const uint2 w0 = *reinterpret_cast<const uint2 *>(w + u.c0);
+                const uint2 w1 = *reinterpret_cast<const uint2 *>(w + u.c1);
+                const uint32_t wh[4] = {w0.x, w0.y, w1.x, w1.y};
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const float2 f = __half22float2(wh[i]);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&wh[i]));
                     v[2 * i] *= inv * f.x;
                     v[2 * i + 1] *= inv * f.y;
                 }
             }
         }
-        if (!live) continue;
-        if (turned) {
+        if (!u.live) continue;
+        if (u.turned) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float2 t = cs[4 * lane + i];
-                const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + 1 : i + 4;
-                const float a = v[ia], b = v[ib];
-                v[ia] = a * t.x - b * t.y;
-                v[ib] = a * t.y + b * t.x;
+                if (p.interleaved) {
+                    const float a = v[2 * i], b = v[2 * i + 1];
+                    v[2 * i] = a * t.x - b * t.y;
+                    v[2 * i + 1] = a * t.y + b * t.x;
+                } else {
+                    const float a = v[i], b = v[i + 4];
+                    v[i] = a * t.x - b * t.y;
+                    v[i + 4] = a * t.y + b * t.x;
+                }
             }
         }
         __half *dst;
-        if (h < p.n_q) {
-            dst = p.q + (m * p.n_q + h) * p.D;
+        if (u.h < p.n_q) {
+            dst = p.q + (m * p.n_q + u.h) * p.D;
         } else {
             if (!cached) continue;
-            const int hk = is_v ? h - p.n_q - p.n_kv : h - p.n_q;
-            dst = (is_v ? p.v : p.k) + slot * p.tok_stride + hk * p.head_stride;
+            const int hk = u.is_v ? u.h - p.n_q - p.n_kv : u.h - p.n_q;
+            dst = (u.is_v ? p.v : p.k) + slot * p.tok_stride + hk * p.head_stride;
         }
         const uint2 lo = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
         const uint2 hi = make_uint2(pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
-        if (c1 == c0 + 4 && !(c0 & 7)) {
-            *reinterpret_cast<uint4 *>(dst + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (u.c1 == u.c0 + 4 && !(u.c0 & 7)) {
+            *reinterpret_cast<uint4 *>(dst + u.c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         } else {
-            *reinterpret_cast<uint2 *>(dst + c0) = lo;
-            *reinterpret_cast<uint2 *>(dst + c1) = hi;
+            *reinterpret_cast<uint2 *>(dst + u.c0) = lo;
+            *reinterpret_cast<uint2 *>(dst + u.c1) = hi;
         }
     }
 }
@@ -183,13 +199,16 @@ extern "C" CQ_API cq_status cq_rope_qkv(const cq_rope_desc *d, int64_t M, const 
     p.eps = d->eps;
     for (p.log2g = 0; (8 << p.log2g) < p.D; p.log2g++) {
     }
-    const int heads = p.n_q + 2 * p.n_kv;
-    p.heads_per_cta = heads;
+    // one CTA a token (the angles once); few tokens: one round of heads a CTA
+    const int heads = p.n_q + 2 * p.n_kv, groups = kRopeThreads >> p.log2g;
+    const int rounds = (heads + groups - 1) / groups;
+    const bool split = M * rounds <= 4LL * sm_count();
+    p.heads_per_cta = split ? groups : heads;
     try {
         cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
         TimedScope ts(st, CQ_KERNEL_ROPE_QKV);
         count_launch();
-        return launch_pdl(k_rope_qkv, dim3((unsigned)M, 1), dim3(kRopeThreads), 0, st, 1, p) ==
+        return launch_pdl(k_rope_qkv, dim3((unsigned)M, split ? rounds : 1), dim3(kRopeThreads), 0, st, 1, p) ==
                        cudaSuccess
                    ? CQ_OK
                    : CQ_ERR_CUDA;
