@@ -120,18 +120,18 @@ CQ_DEV void norm_regs(double (&v)[E], int nv, const NormArgs &a, const __half *w
     for (int c = 0; c < E; c += 8) {
         if (w) {
             double f[8];
-            halves(wv[c / 8], f);
+            halves_tiny(wv[c / 8], f);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[c + i] *= inv * f[i];
+            for (int i = 0; i < 8; i++) v[c + i] *= inv * (f[i] * kHalfUp);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c + i] *= inv;
         }
         if (b && c < nv) {
             double f[8];
-            halves(*reinterpret_cast<const uint4 *>(b + c0 + c), f);
+            halves_tiny(*reinterpret_cast<const uint4 *>(b + c0 + c), f);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[c + i] += f[i];
+            for (int i = 0; i < 8; i++) v[c + i] = fma(f[i], kHalfUp, v[c + i]);
         }
     }
 }
