@@ -77,26 +77,46 @@ CQ_DEV uint4 keep_first(uint4 v, int k) {
 // (2q, 2q + 1) and (2q + 8, 2q + 9), for both operands.
 CQ_DEV uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// What a CTA of the one-launch form works on.
+struct FoundTile {
+    int id, rank, rows, first;  // first: place of the tile's first row among the adapter's rows
+    float scale;
+};
+
 // Row i is thread i's (M <= kLoraThreads).  Rows of an adapter form tiles of TM in
 // row order; the row that begins one leads it, and tile t is that of the t-th
 // leading row.  False if there is none.  buf: 256 ints of shared memory.
-CQ_DEV bool find_tile(const LoraArgs &p, int t, int TM, int *buf, int *s_rows, int *s_id,
-                      int *s_count) {
+CQ_DEV bool find_tile(const LoraArgs &p, int t, int TM, int *buf, int *s_rows, FoundTile *f) {
     __shared__ int s_lead[kLoraWarps];
-    __shared__ int s_first;
     const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-    const bool row = i < p.M;
     // -2: no row, and no adapter where such rows need nothing done (in place)
-    int id = row ? valid_id(p.ids[i], p.n) : -2;
+    int id = i < p.M ? valid_id(p.ids[i], p.n) : -2;
     if (id == -1 && p.y == p.out) id = -2;
     buf[i] = id;
-    if (i == 0) *s_count = 0;
+    // the row's rank and scale come while the tile is looked for
+    int rank = 0;
+    float scale = 1.0f;
+    if (id >= 0) {
+        rank = p.ranks ? max(0, min(p.ranks[id], p.r)) : p.r;
+        if (p.scale) scale = p.scale[id];
+    }
     __syncthreads();
-    int before = __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
+    // rows of the same adapter before this one (comparisons: __match_any takes a step
+    // per different value)
+    int before = 0;
     const int4 *b4 = reinterpret_cast<const int4 *>(buf);
-    for (int j = 0; j < 8 * warp; j++) {
-        const int4 o = b4[j];
-        before += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+    if (32 * warp < p.M) {
+#pragma unroll 8
+        for (int j = 0; j < 8 * warp; j++) {
+            const int4 o = b4[j];
+            before += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int4 o = b4[8 * warp + j];
+            before += (o.x == id && 4 * j < lane) + (o.y == id && 4 * j + 1 < lane) +
+                      (o.z == id && 4 * j + 2 < lane) + (o.w == id && 4 * j + 3 < lane);
+        }
     }
     const bool leads = id != -2 && before % TM == 0;
     const unsigned mask = __ballot_sync(0xffffffffu, leads);
@@ -109,18 +129,15 @@ CQ_DEV bool find_tile(const LoraArgs &p, int t, int TM, int *buf, int *s_rows, i
         total += s_lead[w];
     }
     if (t >= total) return false;
-    if (leads && at == t) {
-        *s_id = id;
-        s_first = before;
-    }
+    if (leads && at == t) *f = FoundTile{id, rank, 0, before, scale};
     __syncthreads();
-    const int place = before - s_first;
-    const bool mine = id == *s_id && place >= 0 && place < TM;
+    const int place = before - f->first;
+    const bool mine = id == f->id && place >= 0 && place < TM;
     if (mine) s_rows[place] = i;
     const int count = __syncthreads_count(mine);
     // the places beyond the last row repeat it (their results are not stored)
     if (i >= count && i < TM) s_rows[i] = s_rows[count - 1];
-    if (i == 0) *s_count = count;
+    if (i == 0) f->rows = count;
     __syncthreads();
     return true;
 }
@@ -502,7 +519,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     __half *tl = th + TM * S::LDT;
     __shared__ int s_rows[TM];
     __shared__ float s_factor[TM];
-    __shared__ int s_id, s_count;
+    __shared__ FoundTile s_tile;
 
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
@@ -512,10 +529,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     griddep_launch();
 
     // ---- the tile: adapter and rows (the same for every CTA of the cluster)
-    if (!find_tile(p, tile, TM, reinterpret_cast<int *>(smem), s_rows, &s_id, &s_count)) return;
-    const int id = s_id, rows = s_count;
-    const int rank = id < 0 ? 0 : p.ranks ? max(0, min(p.ranks[id], p.r)) : p.r;
-    const float sc = id >= 0 && p.scale ? p.scale[id] : 1.0f;
+    if (!find_tile(p, tile, TM, reinterpret_cast<int *>(smem), s_rows, &s_tile)) return;
+    const int id = s_tile.id, rows = s_tile.rows, rank = s_tile.rank;
+    const float sc = s_tile.scale;
 
     // columns of this CTA, in blocks of W
     const int nblk = (p.N + X::W - 1) / X::W;
@@ -824,12 +840,16 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
 #pragma unroll
         for (int u = 0; u < kPlanRows; u++) {
             if (b0 + u * kPlanThreads >= M) break;
-            // the lanes of a warp with the same adapter take one atomic
-            const unsigned peers = __match_any_sync(0xffffffffu, key[u]);
-            const int leader = __ffs(peers) - 1;
-            int base = 0;
-            if (lane == leader && key[u] >= 0) base = atomicAdd(&cnt[key[u]], __popc(peers));
-            at[u] = __shfl_sync(0xffffffffu, base, leader) + __popc(peers & ((1u << lane) - 1u));
+            // a warp inside one request takes one atomic
+            int same;
+            __match_all_sync(0xffffffffu, key[u], &same);
+            if (same) {
+                int base = 0;
+                if (lane == 0 && key[u] >= 0) base = atomicAdd(&cnt[key[u]], 32);
+                at[u] = __shfl_sync(0xffffffffu, base, 0) + lane;
+            } else {
+                at[u] = key[u] >= 0 ? atomicAdd(&cnt[key[u]], 1) : 0;
+            }
             const int i = b0 + u * kPlanThreads + tid;
             if (!once && i < M) place[i] = at[u];
         }
