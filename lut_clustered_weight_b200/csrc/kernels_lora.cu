@@ -348,8 +348,9 @@ CQ_DEV void gather_t(cg::cluster_group &cluster, float *part, int C, int rows, f
 }
 
 // Expansion.  A warp has 16 rows of the tile, whose t it keeps in fragments, and
-// goes over column blocks of 8 NB: MMA column 2q + e of n8 tile j is column
-// 2 NB q + 2j + e of the block, so a lane holds 2 NB consecutive columns of y.
+// goes over column blocks of 8 NB: MMA column 2q + e of n8 tiles 2i and 2i + 1 is
+// column 16 i + 4q + e, + 2 in the second, of the block, so a lane holds 4
+// consecutive columns of y and four lanes 64 bytes of a row.
 template <int R, int NB>
 struct Expand {
     static constexpr int KS = R >= 32 ? R / 32 : 1;   // 32-wide steps of the rank
@@ -386,11 +387,13 @@ struct Expand {
     };
     static constexpr int pieces = NB;  // 16-byte pieces of y a lane has per block and 16 rows
 
+    // the row of B, in the block, that is row g of n8 tile j
+    CQ_DEV static int b_row(int j, int g) { return 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1); }
     CQ_DEV static void load_b(B &o, const LoraArgs &p, int id, int rank, int n0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
 #pragma unroll
         for (int j = 0; j < NB; j++) {
-            const int col = n0 + 2 * NB * (g >> 1) + 2 * j + (g & 1);
+            const int col = n0 + b_row(j, g);
             const __half *br = p.b + ((int64_t)id * p.N + min(col, p.N - 1)) * p.r;
 #pragma unroll
             for (int s = 0; s < KS; s++) {
@@ -409,14 +412,14 @@ struct Expand {
             }
         }
     }
-    // the same from staged rows; row: the one of n8 tile 0 that this lane reads
-    CQ_DEV static void take_b(B &o, const unsigned char *row, int pitch) {
-        const int q = threadIdx.x & 3;
+    // the same from the block's staged rows
+    CQ_DEV static void take_b(B &o, const unsigned char *rows, int pitch) {
+        const int q = threadIdx.x & 3, g = (threadIdx.x & 31) >> 2;
 #pragma unroll
         for (int j = 0; j < NB; j++) {
+            const unsigned char *at = rows + b_row(j, g) * pitch;
 #pragma unroll
             for (int s = 0; s < KS; s++) {
-                const unsigned char *at = row + 2 * j * pitch;
                 if (R >= 32) {
                     o.w[j][s] = *reinterpret_cast<const uint4 *>(at + 64 * s + 16 * q);
                 } else {
@@ -437,15 +440,15 @@ struct Expand {
     }
     // y of a block and 16 rows into this thread's own pieces of a slot (256
     // pieces apart), and from there: no other thread reads them, so no barrier
-    // (ya, yb: y at column 2 NB q of the warp's rows g and g + 8, NULL: no row)
+    // (ya, yb: y at column 4q of the warp's rows g and g + 8, NULL: no row)
     CQ_DEV static void fetch_y(unsigned char *slot, const float *ya, const float *yb, int N, int n0) {
-        const int c = n0 + 2 * NB * (threadIdx.x & 3);
+        const int c = n0 + 4 * (threadIdx.x & 3);
         unsigned char *dst = slot + 16 * threadIdx.x;
 #pragma unroll
         for (int i = 0; i < NB / 2; i++) {
-            const bool in = c + 4 * i < N;  // N % 8 == 0
-            if (in && ya) cp_async16_zfill(dst + 2 * i * 16 * kLoraThreads, ya + n0 + 4 * i, 16);
-            if (in && yb) cp_async16_zfill(dst + (2 * i + 1) * 16 * kLoraThreads, yb + n0 + 4 * i, 16);
+            const bool in = c + 16 * i < N;  // N % 8 == 0
+            if (in && ya) cp_async16_zfill(dst + 2 * i * 16 * kLoraThreads, ya + n0 + 16 * i, 16);
+            if (in && yb) cp_async16_zfill(dst + (2 * i + 1) * 16 * kLoraThreads, yb + n0 + 16 * i, 16);
         }
     }
     CQ_DEV static void take_y(Y &o, const unsigned char *slot) {
@@ -458,7 +461,7 @@ struct Expand {
     }
     CQ_DEV static void run(const B &w, const T &t, const Y &y, float fa, float fb, float *oa,
                            float *ob, int N, int n0) {
-        const int c = n0 + 2 * NB * (threadIdx.x & 3);
+        const int c = n0 + 4 * (threadIdx.x & 3);
         float acc[NB][4];
 #pragma unroll
         for (int j = 0; j < NB; j++)
@@ -481,13 +484,13 @@ struct Expand {
 #pragma unroll
         for (int i = 0; i < NB / 2; i++) {
             const float(&l)[4] = acc[2 * i], (&h)[4] = acc[2 * i + 1];
-            if (c + 4 * i < N) {
+            if (c + 16 * i < N) {
                 if (oa)
-                    reinterpret_cast<float4 *>(oa + n0)[i] =
+                    *reinterpret_cast<float4 *>(oa + n0 + 16 * i) =
                         make_float4(y.a[i].x + fa * l[0], y.a[i].y + fa * l[1], y.a[i].z + fa * h[0],
                                     y.a[i].w + fa * h[1]);
                 if (ob)
-                    reinterpret_cast<float4 *>(ob + n0)[i] =
+                    *reinterpret_cast<float4 *>(ob + n0 + 16 * i) =
                         make_float4(y.b[i].x + fb * l[2], y.b[i].y + fb * l[3], y.b[i].z + fb * h[2],
                                     y.b[i].w + fb * h[3]);
             }
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     static_assert(D >= 1, "no room for y");
     constexpr int MB = TM / 16, WC = kLoraWarps / MB;  // warps along the rows, along the columns
     unsigned char *slots = smem + y_off;
-    const int ra = 16 * (warp % MB) + g, rb = ra + 8, cq = 2 * NB * (lane & 3);
+    const int ra = 16 * (warp % MB) + g, rb = ra + 8, cq = 4 * (lane & 3);
     const bool busy = 16 * (warp % MB) < rows;
     const float *ya = ra < rows ? p.y + (int64_t)s_rows[ra] * p.ldy + cq : nullptr;
     const float *yb = rb < rows ? p.y + (int64_t)s_rows[rb] * p.ldy + cq : nullptr;
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_t(const LoraArgs p) {
 // t; the tile past the L1, which may hold an earlier call's.
 template <int TM, int R>
 struct OutShape {
-    static constexpr int NB = 2;                           // n8 tiles of a warp's step
+    static constexpr int NB = TM == 64 && R <= 64 ? 4 : 2;    // n8 tiles of a warp's step
     static constexpr int MB = TM / 16, WC = kLoraWarps / MB;  // warps along the rows, along the columns
     static constexpr int W = WC * 8 * NB;                  // columns of a step
     // bytes of a staged row of B: the 8 rows of a fragment load hit different banks
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) 
     const int ra = 16 * (warp % S::MB) + g, rb = ra + 8, wc = warp / S::MB;
     const int cw = wc * X::W;                   // the warp's columns in a step
     const bool busy = 16 * (warp % S::MB) < rows;
-    const int cq = 2 * S::NB * q;
+    const int cq = 4 * q;
     const float *ya = ra < rows ? p.y + (int64_t)s_rows[ra] * p.ldy + cq : nullptr;
     const float *yb = rb < rows ? p.y + (int64_t)s_rows[rb] * p.ldy + cq : nullptr;
     float *oa = ra < rows ? p.out + (int64_t)s_rows[ra] * p.ldo + cq : nullptr;
@@ -758,7 +761,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) 
         if (busy) {
             const unsigned char *st = smem + slot * S::stage;
             typename X::B w;
-            X::take_b(w, st + (cw + 4 * (g >> 1) + (g & 1)) * S::pitch, S::pitch);
+            X::take_b(w, st + cw * S::pitch, S::pitch);
             X::cut_b(w, rank);
             typename X::Y y;
             X::take_y(y, st + S::y_off);
