@@ -40,7 +40,7 @@ constexpr int kLoraMaxRank = 128;
 constexpr int kLoraSmallM = kLoraThreads;
 
 struct LoraTile {
-    int id, start, rows, pad;  // rows perm[start, start + rows); id -1: no adapter
+    int id, start, rows, rank;  // id -1: no adapter; start: of its rows among the sorted ones
 };
 
 struct LoraArgs {
@@ -56,7 +56,7 @@ struct LoraArgs {
     // planned launches only (M > kLoraSmallM)
     const int *n_tiles;
     const LoraTile *tiles;
-    const int *perm;
+    const int *list;  // rows of tile i at list[i * TM ..)
     __half *t;        // [2][M][R]: hi, lo of the sorted rows
     float *factor;    // [M]
     int splits;       // CTAs a tile's columns are shared out to (k_lora_out)
@@ -153,7 +153,7 @@ struct LoraShape {
     // halves a row of hi / lo: 8 rows of a fragment load hit different banks (16-byte
     // loads: rows 64 bytes apart modulo 128; R 16, 8-byte loads: 32)
     static constexpr int LDT = R <= 32 ? R : R + 32;
-    static constexpr int t_bytes = 2 * TM * LDT * 2;      // hi, lo
+    static constexpr int t_bytes = TM == 16 ? 2 * TM * LDT * 2 : 0;  // hi, lo (k_lora only)
     static constexpr int fit = (110 * 1024 - t_bytes) / stage;   // two CTAs an SM
     static constexpr int NS = fit > 4 ? 4 : fit < 2 ? 2 : fit;   // stages
     static constexpr int WK = TM == 16 ? kLoraWarps : 1;  // partial t of a CTA (warps along k)
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     int slot = 0;
     for (; nb < nb1; nb += WC) {
         if (nb + WC < nb1) X::load_b(wn, p, id, rank, (nb + WC) * X::W);
-        X::cut_b(w, rank);
+        if (rank & 7) X::cut_b(w, rank);
         typename X::Y y;
         cp_async_wait_group<D - 1>();
         X::take_y(y, slots + slot * slot_bytes);
@@ -613,18 +613,17 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
 // shrink is short and waits on latencies, its expansion streams y, and in one
 // launch all CTAs would be in the same phase at the same time (4096 rows, K 2048,
 // N 2816, rank 64: 20 of 45 us with y on its way).
+// The tile's entry and rows, by loads that do not wait for one another and go past
+// the L1 (k_lora_out reads them before its wait, and an earlier call may have left its
+// own there).  s_rows beyond the tile's rows is not meaningful.
 template <int TM>
 CQ_DEV bool planned_tile(const LoraArgs &p, int tile, int *s_rows, LoraTile &T) {
-    if (tile >= __ldcg(p.n_tiles)) return false;
+    const int n = __ldcg(p.n_tiles);
     const int4 v = __ldcg(reinterpret_cast<const int4 *>(p.tiles + tile));
+    if (threadIdx.x < TM) s_rows[threadIdx.x] = __ldcg(p.list + (int64_t)tile * TM + threadIdx.x);
     T = LoraTile{v.x, v.y, v.z, v.w};
-    if (threadIdx.x < TM)
-        s_rows[threadIdx.x] = __ldcg(p.perm + T.start + min((int)threadIdx.x, T.rows - 1));
     __syncthreads();
-    return true;
-}
-CQ_DEV int rank_of(const LoraArgs &p, int id) {
-    return id < 0 ? 0 : p.ranks ? max(0, min(__ldcg(p.ranks + id), p.r)) : p.r;
+    return tile < n;
 }
 
 // t = A x of a tile by a cluster: the CTAs split K, then each sums the partial t of
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_t(const LoraArgs p) {
     griddep_launch();
     LoraTile T;
     if (!planned_tile<TM>(p, blockIdx.x / C, s_rows, T)) return;
-    const int rank = rank_of(p, T.id);
+    const int rank = T.rank;
     if (rank == 0) return;
     const float sc = p.scale ? p.scale[T.id] : 1.0f;
     const int chunks = (p.K + S::KC - 1) / S::KC;
@@ -650,36 +649,53 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_t(const LoraArgs p) {
     cluster.sync();
     constexpr int PER = (R + 31) / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int row = crank * kLoraWarps + warp; row < T.rows; row += C * kLoraWarps) {
-        float v[PER];
+    // a warp's rows, RB of them in flight
+    constexpr int RB = TM == 64 ? 2 : 1;  // (C 4 and 8: TM rows are C * 8 * RB)
+    float v[RB][PER];
 #pragma unroll
-        for (int i = 0; i < PER; i++) v[i] = 0.0f;
-        for (int c = 0; c < C; c += 4) {  // C is a multiple of 4
-            float u[4][PER];
+    for (int b = 0; b < RB; b++)
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const float *rp = cluster.map_shared_rank(part, c + k) + row * S::LDP;
+        for (int i = 0; i < PER; i++) v[b][i] = 0.0f;
+    const int r0 = crank * kLoraWarps + warp;
+    for (int c = 0; c < C; c += 4) {  // C is a multiple of 4
+        float u[4][RB][PER];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float *rp = cluster.map_shared_rank(part, c + k);
+#pragma unroll
+            for (int b = 0; b < RB; b++) {
+                const int row = r0 + b * C * kLoraWarps;
 #pragma unroll
                 for (int i = 0; i < PER; i++)
-                    u[k][i] = R >= 32 || lane < R ? rp[lane + 32 * i] : 0.0f;
+                    u[k][b][i] = row < T.rows && (R >= 32 || lane < R)
+                                     ? rp[row * S::LDP + lane + 32 * i]
+                                     : 0.0f;
             }
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-#pragma unroll
-                for (int i = 0; i < PER; i++) v[i] += u[k][i];
         }
-        const int64_t at = T.start + row;
-        split_row<R>(v, sc, p.t + at * R, p.t + ((int64_t)p.M + at) * R, p.factor + at);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+#pragma unroll
+                for (int i = 0; i < PER; i++) v[b][i] += u[k][b][i];
     }
-    cluster.sync();  // no CTA leaves while another may read its partial t
+    cluster.barrier_arrive();  // this CTA has read every partial t
+#pragma unroll
+    for (int b = 0; b < RB; b++) {
+        const int row = r0 + b * C * kLoraWarps;
+        const int64_t at = T.start + row;
+        if (row < T.rows)
+            split_row<R>(v[b], sc, p.t + at * R, p.t + ((int64_t)p.M + at) * R, p.factor + at);
+    }
+    __syncwarp();
+    cluster.barrier_wait();  // no CTA leaves while another may read its partial t
 }
 
 // out = y + factor * B t of a tile's share of the columns.  A warp has 16 rows of the
 // tile and a share of the columns of each step; a ring of stages holds a step's rows
 // of B (shared by the warps of the same columns) and its y (every thread its own).
 // Nothing before k_lora_t can still be running when this kernel starts (k_lora_t lets it
-// start after its own wait), so the tile, y and B are requested before the wait for
-// t; the tile past the L1, which may hold an earlier call's.
+// start after its own wait), so the tile, y and B are requested before the wait for t.
 template <int TM, int R>
 struct OutShape {
     static constexpr int NB = TM == 64 && R <= 64 ? 4 : 2;    // n8 tiles of a warp's step
@@ -705,7 +721,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) 
         griddep_wait();  // this kernel ends after k_lora_t, whatever its CTAs had to do
         return;
     }
-    const int rows = T.rows, rank = rank_of(p, T.id);
+    const int rows = T.rows, rank = T.rank;
     const int nblk = (p.N + S::W - 1) / S::W;
     const int nb0 = (int)((int64_t)split * nblk / p.splits);
     const int nb1 = (int)((int64_t)(split + 1) * nblk / p.splits);
@@ -762,7 +778,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) 
             const unsigned char *st = smem + slot * S::stage;
             typename X::B w;
             X::take_b(w, st + cw * S::pitch, S::pitch);
-            X::cut_b(w, rank);
+            if (rank & 7) X::cut_b(w, rank);
             typename X::Y y;
             X::take_y(y, st + S::y_off);
             X::run(w, t, y, fa, fb, oa, ob, p.N, nb * S::W + cw);
@@ -773,8 +789,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) 
 }
 
 // ---------------------------------------------------------------- rows by adapter
-// One CTA: counts per adapter (slot n: no adapter), their offsets, the tile
-// list and the permutation.  A row's place among its adapter's rows comes from
+// One CTA: counts per adapter (slot n: no adapter), their offsets, the tiles and
+// their rows.  A row's place among its adapter's rows comes from
 // the counting atomics: their order may change from call to call, and with it the
 // rows of a tile, but a row's result does not depend on its place.
 constexpr int kPlanThreads = 1024;
@@ -817,7 +833,7 @@ CQ_DEV void scan_pair(int &a, int &b, int &ta, int &tb, int (*wsum)[32]) {
 
 __global__ void __launch_bounds__(kPlanThreads)
 k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_none, int *n_tiles,
-            LoraTile *tiles, int *perm, int *place) {
+            LoraTile *tiles, int *list, int *place, const int32_t *__restrict__ ranks, int r_max) {
     extern __shared__ int cnt[];  // [n + 1] counts, then offsets
     __shared__ int wsum[2][32];
     griddep_wait();
@@ -835,6 +851,8 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
             if (key[u] == -1) key[u] = n;
     };
     load(0);
+    auto rank_of = [&](int i) { return i >= n ? 0 : ranks ? max(0, min(ranks[i], r_max)) : r_max; };
+    const int rank0 = rank_of(tid);
     for (int i = tid; i <= n; i += kPlanThreads) cnt[i] = 0;
     __syncthreads();
     const bool once = M <= kPlanRows * kPlanThreads;  // keys and places stay in registers
@@ -866,9 +884,10 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
         int start = c, first = t;
         scan_pair(start, first, rows, nt, wsum);
         if (i <= n) {
-            cnt[i] = start;
+            cnt[i] = first * TM;  // its tiles' places in the list
+            const int rank = b0 ? rank_of(i) : rank0;
             for (int k = 0; k < t; k++)
-                tiles[first + k] = LoraTile{i == n ? -1 : i, start + k * TM, min(TM, c - k * TM), 0};
+                tiles[first + k] = LoraTile{i == n ? -1 : i, start + k * TM, min(TM, c - k * TM), rank};
         }
     }
     if (tid == 0) *n_tiles = nt;
@@ -878,7 +897,8 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
 #pragma unroll
         for (int u = 0; u < kPlanRows; u++) {
             const int i = b0 + u * kPlanThreads + tid;
-            if (i < M) perm[cnt[key[u]] + (once ? at[u] : place[i])] = i;
+            if (i < M && !(skip_none && key[u] == n))
+                list[cnt[key[u]] + (once ? at[u] : place[i])] = i;
         }
     }
 }
@@ -893,15 +913,15 @@ static int64_t lora_max_tiles(int64_t M, int64_t n) {
     return M / lora_tile_rows(M) + std::min(n + 1, M);
 }
 static int lora_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
-// Scratch of a planned call: tile count, tile list, permutation, places, t, factors.
+// Scratch of a planned call: tile count, tiles, their rows, places, t, factors.
 struct LoraScratch {
-    size_t tiles, perm, place, t, factor, total;
+    size_t tiles, list, place, t, factor, total;
 };
 static LoraScratch lora_scratch(int64_t M, int64_t n, int64_t r) {
     LoraScratch s{};
     s.tiles = 256;
-    s.perm = s.tiles + align256(lora_max_tiles(M, n) * sizeof(LoraTile));
-    s.place = s.perm + align256(M * sizeof(int));
+    s.list = s.tiles + align256(lora_max_tiles(M, n) * sizeof(LoraTile));
+    s.place = s.list + align256(lora_max_tiles(M, n) * lora_tile_rows(M) * sizeof(int));
     s.t = s.place + (M > kPlanRows * kPlanThreads ? align256(M * sizeof(int)) : 0);
     s.factor = s.t + align256(2 * M * lora_rank(r) * sizeof(__half));
     s.total = s.factor + align256(M * sizeof(float));
@@ -947,16 +967,16 @@ static cudaError_t launch_lora(LoraArgs p, void *ws, cudaStream_t st) {
     uint8_t *w = reinterpret_cast<uint8_t *>(ws);
     int *n_tiles = reinterpret_cast<int *>(w);
     LoraTile *list = reinterpret_cast<LoraTile *>(w + s.tiles);
-    int *perm = reinterpret_cast<int *>(w + s.perm), *place = reinterpret_cast<int *>(w + s.place);
+    int *rows = reinterpret_cast<int *>(w + s.list), *place = reinterpret_cast<int *>(w + s.place);
     const int TM = lora_tile_rows(p.M);
     count_launch();
     cudaError_t e = launch_pdl(k_lora_plan, dim3(1), dim3(kPlanThreads),
                                (size_t)(p.n + 1) * sizeof(int), st, 1, p.ids, p.M, p.n, TM,
-                               p.y == p.out, n_tiles, list, perm, place);
+                               p.y == p.out, n_tiles, list, rows, place, p.ranks, p.r);
     if (e != cudaSuccess) return e;
     p.n_tiles = n_tiles;
     p.tiles = list;
-    p.perm = perm;
+    p.list = rows;
     p.t = reinterpret_cast<__half *>(w + s.t);
     p.factor = reinterpret_cast<float *>(w + s.factor);
     if (TM == 16)
