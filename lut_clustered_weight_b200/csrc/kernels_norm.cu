@@ -449,7 +449,6 @@ __global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(co
     const int qmax = (1 << (a.bits - 1)) - 1;
     const long long Ai = __double2ll_rn(A * 16777216.0);
     const double R = Ai > 0 ? (double)qmax * recip(A) : 0.0;
-    if (j == 0 && mine) a.s[t] = Ai > 0 ? quant_scale(A, lb, qmax) : 0.0f;
     int8_t *cb = reinterpret_cast<int8_t *>(xch);
     if (mine) {
         if (n2 == 0) {
@@ -479,6 +478,8 @@ __global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(co
                     prmt(nibbles(u.x), nibbles(u.y), 0x6420);
         }
     }
+    // last: two fp64 divisions and a root of one thread, nobody waits for them
+    if (j == 0 && mine) a.s[t] = Ai > 0 ? quant_scale(A, lb, qmax) : 0.0f;
 }
 
 template <int E>
