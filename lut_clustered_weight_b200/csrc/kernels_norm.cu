@@ -27,7 +27,7 @@ struct NormArgs {
     uint8_t *q;
     float *s;
     int64_t ldq, T;
-    double eps, resid_scale, block_scale, inv_h;
+    double eps, resid_scale, block_scale, inv_h, sqrt_b;
     int H, layer, post_norm, gate_mode, bits, log2b;
     int tpr, rpc;  // threads per row (a multiple of 32), rows per CTA
 };
@@ -449,6 +449,9 @@ __global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(co
     const int qmax = (1 << (a.bits - 1)) - 1;
     const long long Ai = __double2ll_rn(A * 16777216.0);
     const double R = Ai > 0 ? (double)qmax * recip(A) : 0.0;
+    // the steps of quant_scale, its root taken on the host
+    if (j == 0 && mine)
+        a.s[t] = __double2float_rn(__ddiv_rn(__ddiv_rn(A, a.sqrt_b), (double)qmax));
     int8_t *cb = reinterpret_cast<int8_t *>(xch);
     if (mine) {
         if (n2 == 0) {
@@ -478,8 +481,6 @@ __global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(co
                     prmt(nibbles(u.x), nibbles(u.y), 0x6420);
         }
     }
-    // last: two fp64 divisions and a root of one thread, nobody waits for them
-    if (j == 0 && mine) a.s[t] = Ai > 0 ? quant_scale(A, lb, qmax) : 0.0f;
 }
 
 template <int E>
@@ -577,6 +578,7 @@ extern "C" CQ_API cq_status cq_residual_norm(const cq_norm_desc *d, int64_t T, c
     a.bits = d->act_bits;
     for (a.log2b = 0; (1 << a.log2b) < b; a.log2b++) {
     }
+    a.sqrt_b = std::sqrt((double)(b > 0 ? b : 1));
     try {
         return launch_residual_norm(a, d->resid_bits == 16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                    ? CQ_OK
