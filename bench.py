@@ -707,7 +707,10 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
     cq_rotate_quantize + cq_lut_gemm, the SwiGLU FFN through cq_moe_ffn, A4W4)
     and once all in bf16 (torch F.linear).  RMSNorm, rotary embedding and
     attention (torch scaled_dot_product_attention) are the same torch code in
-    both, in fp16 / bf16.  Weights are random (the work does not depend on
+    both, in fp16 / bf16.  A third step ("lut_ops") is the LUT one with the norms,
+    residual adds, rotary positions and cache rows through cq_residual_norm (which
+    also makes the QKV product's codes) and cq_rope_qkv; its attention is the same
+    torch call.  Weights are random (the work does not depend on
     their values); each of the n_layers layers has its own, so a step streams
     more than the L2.  Both steps are replayed from CUDA graphs."""
     import torch
@@ -758,6 +761,8 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
                 kc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).half(),
                 vc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).half(),
                 n1=torch.ones(H, device=dev), n2=torch.ones(H, device=dev),
+                w1=torch.ones(H, dtype=torch.float16, device=dev),
+                w2=torch.ones(H, dtype=torch.float16, device=dev),
                 y=torch.empty((M, H), dtype=torch.float32, device=dev)))
             bf_layers.append(dict(
                 wqkv=(torch.randn((nqkv, H), device=dev, generator=g) * 0.02).bfloat16(),
@@ -782,6 +787,33 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
                 x = x1 + L["y"].half()
             return x
 
+        # the cache's rows as cq_rope_qkv addresses them: token stride hd, head stride
+        # (ctx + 1) hd, sequence m's new token at row m nkv (ctx + 1) + ctx
+        positions = torch.full((M,), ctx, dtype=torch.int32, device=dev)
+        slots = torch.arange(M, device=dev) * (nkv * (ctx + 1)) + ctx
+        freq = torch.from_numpy(cq.rope_inv_freq(hd, 1e6)).to(dev)
+
+        def cache_rows(c):
+            rows = c.numel() // hd - (nkv - 1) * (ctx + 1)
+            return c.as_strided((rows, nkv, hd), (hd, (ctx + 1) * hd, 1))
+
+        def ops_step():
+            r, y = x_lut, None
+            for L in lut_layers:
+                r, _, qc, sq = cq.cq_residual_norm(r, y, pre_weight=L["w1"], had_block=512,
+                                                   act_bits=4)
+                qkv = cq.cq_lut_gemm(qc, sq, H, 4, L["wqkv"], L["cqkv"])
+                q, _, _ = cq.cq_rope_qkv(qkv, positions, freq, nq, nkv, head_dim=hd,
+                                         k_out=cache_rows(L["kc"]), v_out=cache_rows(L["vc"]),
+                                         slots=slots)
+                a = F.scaled_dot_product_attention(q.view(M, nq, 1, hd), L["kc"], L["vc"],
+                                                   enable_gqa=True)
+                oc, so = cq.cq_rotate_quantize(a.reshape(M, nq * hd), 4096, 4)
+                o = cq.cq_lut_gemm(oc, so, nq * hd, 4, L["wo"], L["co"])
+                r, x1 = cq.cq_residual_norm(r, o, pre_weight=L["w2"])
+                y = L["ffn"](x1, None, L["y"])
+            return r, y
+
         def bf_step():
             x = x_bf
             for L in bf_layers:
@@ -793,7 +825,7 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
             return x
 
         res = {}
-        for nm, fn in (("lut", lut_step), ("bf16", bf_step)):
+        for nm, fn in (("lut", lut_step), ("lut_ops", ops_step), ("bf16", bf_step)):
             for _ in range(args.warmup):
                 fn()
             torch.cuda.synchronize()
@@ -807,12 +839,15 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
                        "ms_per_step": ms / args.steps}
             del graph
         out[f"M{M}"] = {**res, "speedup_vs_bf16": res["lut"]["tokens_per_s"] /
+                        res["bf16"]["tokens_per_s"],
+                        "lut_ops_speedup_vs_bf16": res["lut_ops"]["tokens_per_s"] /
                         res["bf16"]["tokens_per_s"]}
         del lut_layers, bf_layers
         torch.cuda.empty_cache()
     out["config"] = {"model": "Qwen3-4B-shaped decoder layers (random weights)",
                      "layers_per_step": n_layers, "kv_context": ctx, "heads": [nq, nkv, hd],
                      "lut": "A4W4, QKV / O / FFN through the C ABI; attention torch fp16",
+                     "lut_ops": "as lut, with cq_residual_norm and cq_rope_qkv",
                      "bf16": "torch F.linear, attention torch bf16"}
     return out
 

@@ -421,6 +421,31 @@ def test_rope_qkv_keeps_the_dot_product_of_equal_distances(cq):
     assert max(d) - min(d) <= 2 * (2.0 ** -10 + 1e-5) * size
 
 
+def test_rope_qkv_into_a_cache_of_sequences(cq):
+    """A cache [sequence, head, token, channel]: token stride D, head stride
+    tokens * D, and sequence m's token p at row m * heads * tokens + p of a strided
+    view (the decoder-layer leg of bench.py writes its cache so)."""
+    M, nq, nkv, D, ctx = 5, 4, 2, 32, 7
+    g = np.random.default_rng(3)
+    qkv = _dev(g.standard_normal((M, (nq + 2 * nkv) * D)).astype(np.float32))
+    pos = g.integers(0, ctx, M).astype(np.int32)
+    freq = _dev(cq.rope_inv_freq(D))
+    q0, k0, v0 = cq.cq_rope_qkv(qkv, _dev(pos), freq, nq, nkv, head_dim=D)
+    kc = torch.full((M, nkv, ctx, D), 5.0, dtype=torch.float16, device=DEV)
+    vc = torch.full_like(kc, 6.0)
+
+    def rows(c):
+        return c.as_strided((M * nkv * ctx - (nkv - 1) * ctx, nkv, D), (D, ctx * D, 1))
+
+    slots = torch.arange(M, device=DEV) * (nkv * ctx) + _dev(pos.astype(np.int64))
+    q1, _, _ = cq.cq_rope_qkv(qkv, _dev(pos), freq, nq, nkv, head_dim=D, k_out=rows(kc),
+                              v_out=rows(vc), slots=slots)
+    want_k, want_v = torch.full_like(kc, 5.0), torch.full_like(kc, 6.0)
+    for m in range(M):
+        want_k[m, :, pos[m]], want_v[m, :, pos[m]] = k0[m], v0[m]
+    assert torch.equal(q0, q1) and torch.equal(kc, want_k) and torch.equal(vc, want_v)
+
+
 def test_rope_qkv_refusals(cq):
     qkv = torch.zeros((2, 64), device=DEV)
     pos = torch.zeros(2, dtype=torch.int32, device=DEV)
