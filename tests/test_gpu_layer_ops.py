@@ -108,6 +108,12 @@ NORM_CASES = [
     (400, 8192, "rms", 32, True, True, "channel", 1.0, 1.0, 4096, 8),
     (320, 2304, "layer", 16, True, False, "none", 1.0, 1.0, 256, 8),
     (310, 16384, "rms", 16, True, False, "none", 1.0, 1.0, 16, 4),
+    # the last thread of a row has 8 channels less
+    (3, 8200, "rms", 16, True, True, "element", 1.0, 1.0, 8, 4),
+    (300, 8216, "layer", 32, True, False, "none", 1.0, 1.0, 4, 8),
+    (298, 4104, "rms", 32, True, True, "channel", 1.0, 1.0, 2, 8),
+    # a mean far from the spread
+    (310, 1000, "layer", 32, True, True, "none", 1.0, 1e4, 0, 0),
 ]
 
 
@@ -133,7 +139,9 @@ def test_residual_norm_is_the_rounded_definition(cq, T, H, kind, rb, block, post
 @pytest.mark.parametrize("T,H", [(3, 512), (400, 1024)])
 def test_residual_norm_codes_are_cq_rotate_quantize_of_x(cq, T, H):
     d = _norm_inputs(T, H, "rms", 16, True, True, "token", seed=5)
-    for had in (1, 4, 32, 256, 512):
+    for had in (1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 1024):
+        if had > H:
+            continue
         for bits in (4, 8):
             _, x, q, s = _norm_run(cq, d, "rms", 1.0, 1.0, had, bits)
             q2, s2 = cq.cq_rotate_quantize(x, had, bits)
