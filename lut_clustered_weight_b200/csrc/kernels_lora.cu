@@ -796,7 +796,24 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_out(const LoraArgs p) 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 8;  // rows a thread holds at once
 
-// Exclusive scan over the CTA of (a, b); adds and advances the running totals.
+// Exclusive scan over a warp, and over the CTA, of (a, b); adds and advances the running
+// totals.
+CQ_DEV void warp_scan_pair(int &a, int &b, int &ta, int &tb) {
+    const int lane = threadIdx.x & 31, a0 = a, b0 = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+            a += x;
+            b += y;
+        }
+    }
+    const int sa = __shfl_sync(0xffffffffu, a, 31), sb = __shfl_sync(0xffffffffu, b, 31);
+    a += ta - a0;
+    b += tb - b0;
+    ta += sa;
+    tb += sb;
+}
 CQ_DEV void scan_pair(int &a, int &b, int &ta, int &tb, int (*wsum)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int a0 = a, b0 = b;
@@ -834,7 +851,9 @@ CQ_DEV void scan_pair(int &a, int &b, int &ta, int &tb, int (*wsum)[32]) {
 __global__ void __launch_bounds__(kPlanThreads)
 k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_none, int *n_tiles,
             LoraTile *tiles, int *list, int *place, const int32_t *__restrict__ ranks, int r_max) {
-    extern __shared__ int cnt[];  // [n + 1] counts, then offsets
+    extern __shared__ int cnt[];  // [n + 1] counts, then places in the list
+    int *row0 = cnt + n + 1;      // [n + 1] first sorted row of each adapter
+    int *tile0 = row0 + n + 1;    // [n + 2] first tile
     __shared__ int wsum[2][32];
     griddep_wait();
     griddep_launch();
@@ -851,8 +870,6 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
             if (key[u] == -1) key[u] = n;
     };
     load(0);
-    auto rank_of = [&](int i) { return i >= n ? 0 : ranks ? max(0, min(ranks[i], r_max)) : r_max; };
-    const int rank0 = rank_of(tid);
     for (int i = tid; i <= n; i += kPlanThreads) cnt[i] = 0;
     __syncthreads();
     const bool once = M <= kPlanRows * kPlanThreads;  // keys and places stay in registers
@@ -876,22 +893,44 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
         }
     }
     __syncthreads();
+    // prefixes of rows and tiles over the adapters: one warp's scan up to 31 of them
     int rows = 0, nt = 0;
     for (int b0 = 0; b0 <= n; b0 += kPlanThreads) {
         const int i = b0 + tid;
         const int c = i <= n ? cnt[i] : 0;
         const int t = i == n && skip_none ? 0 : (c + TM - 1) / TM;
         int start = c, first = t;
-        scan_pair(start, first, rows, nt, wsum);
+        if (n >= 32)
+            scan_pair(start, first, rows, nt, wsum);
+        else if (tid < 32)
+            warp_scan_pair(start, first, rows, nt);
         if (i <= n) {
             cnt[i] = first * TM;  // its tiles' places in the list
-            const int rank = b0 ? rank_of(i) : rank0;
-            for (int k = 0; k < t; k++)
-                tiles[first + k] = LoraTile{i == n ? -1 : i, start + k * TM, min(TM, c - k * TM), rank};
+            row0[i] = start;
+            tile0[i] = first;
+            if (i == n) tile0[n + 1] = first + t;
         }
     }
-    if (tid == 0) *n_tiles = nt;
     __syncthreads();
+    nt = tile0[n + 1];
+    if (tid == 0) *n_tiles = nt;
+    for (int ti = tid; ti < nt; ti += kPlanThreads) {
+        // the adapter whose tiles hold ti: the last with tile0 <= ti (those without
+        // tiles have the next one's tile0)
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tile0[mid] <= ti)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int k = ti - tile0[lo];
+        const int rank = lo == n ? 0 : ranks ? max(0, min(ranks[lo], r_max)) : r_max;
+        const int here = row0[lo] + k * TM;
+        const int end = lo == n ? M : row0[lo + 1];
+        tiles[ti] = LoraTile{lo == n ? -1 : lo, here, min(TM, end - here), rank};
+    }
     for (int b0 = 0; b0 < M; b0 += kPlanRows * kPlanThreads) {
         if (!once) load(b0);
 #pragma unroll
@@ -971,7 +1010,7 @@ static cudaError_t launch_lora(LoraArgs p, void *ws, cudaStream_t st) {
     const int TM = lora_tile_rows(p.M);
     count_launch();
     cudaError_t e = launch_pdl(k_lora_plan, dim3(1), dim3(kPlanThreads),
-                               (size_t)(p.n + 1) * sizeof(int), st, 1, p.ids, p.M, p.n, TM,
+                               (size_t)(3 * p.n + 4) * sizeof(int), st, 1, p.ids, p.M, p.n, TM,
                                p.y == p.out, n_tiles, list, rows, place, p.ranks, p.r);
     if (e != cudaSuccess) return e;
     p.n_tiles = n_tiles;
