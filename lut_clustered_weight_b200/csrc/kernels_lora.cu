@@ -979,7 +979,10 @@ static cudaError_t launch_small(const LoraArgs &p, cudaStream_t st) {
 
 template <int TM, int R>
 static cudaError_t launch_planned(LoraArgs p, cudaStream_t st) {
-    constexpr int C = TM == 16 ? 8 : 4;
+    // K over 8 CTAs instead of 4 where a CTA's part is still 16 stages or more and the
+    // sums to be exchanged are small (2442 rows, K 6448, rank 16: 23.5 us, and 27.7
+    // with 4; 4096 rows, K 2048, rank 64: 41 and 34)
+    const int C = R <= 32 && p.K >= 64 * LoraShape<TM, R>::KC ? 8 : 4;
     const int64_t tiles = lora_max_tiles(p.M, p.n);
     count_launch(2);
     cudaError_t e = launch_pdl(k_lora_t<TM, R>, dim3((unsigned)(tiles * C)), dim3(kLoraThreads),
