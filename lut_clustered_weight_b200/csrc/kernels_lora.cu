@@ -500,13 +500,25 @@ struct Expand {
 
 // out = y for the columns [c0, c1) of a tile without an adapter.
 CQ_DEV void copy_rows(const LoraArgs &p, const int *s_rows, int rows, int c0, int c1) {
-    if (p.y == p.out) return;
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < rows; i += kLoraWarps) {
-        const float *src = p.y + (int64_t)s_rows[i] * p.ldy;
-        float *dst = p.out + (int64_t)s_rows[i] * p.ldo;
-        for (int c = c0 + 4 * lane; c < c1; c += 128)
-            *reinterpret_cast<float4 *>(dst + c) = *reinterpret_cast<const float4 *>(src + c);
+    if (p.y == p.out || c1 <= c0) return;
+    constexpr int U = 4;  // pieces of 4 columns a thread has on their way
+    const int per = (c1 - c0) >> 2, total = rows * per;
+    for (int i0 = threadIdx.x; i0 < total; i0 += U * kLoraThreads) {
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int i = i0 + u * kLoraThreads, row = i / per;
+            if (i < total)
+                v[u] = *reinterpret_cast<const float4 *>(p.y + (int64_t)s_rows[row] * p.ldy + c0 +
+                                                         4 * (i - row * per));
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int i = i0 + u * kLoraThreads, row = i / per;
+            if (i < total)
+                *reinterpret_cast<float4 *>(p.out + (int64_t)s_rows[row] * p.ldo + c0 +
+                                            4 * (i - row * per)) = v[u];
+        }
     }
 }
 
