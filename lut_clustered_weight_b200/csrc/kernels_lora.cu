@@ -146,7 +146,10 @@ CQ_DEV void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];"
 
 template <int TM, int R>
 struct LoraShape {
-    static constexpr int KC = TM == 64 ? 64 : 128;        // k of a stage
+    static constexpr int WM = TM / 16;                    // warps along the rows
+    static constexpr int WN = TM == 64 || R == 128 ? 2 : 1;  // along the rank
+    static constexpr int WK = kLoraWarps / WM / WN;       // along k: partial t of a CTA
+    static constexpr int KC = TM == 64 ? 64 : 16 * WK;    // k of a stage
     static constexpr int pitch = 2 * KC + 16;             // bytes of a staged row (ldmatrix: no conflicts)
     static constexpr int rows = TM + R;                   // x rows, then A rows
     static constexpr int stage = rows * pitch;
@@ -156,7 +159,6 @@ struct LoraShape {
     static constexpr int t_bytes = TM == 16 ? 2 * TM * LDT * 2 : 0;  // hi, lo (k_lora only)
     static constexpr int fit = (110 * 1024 - t_bytes) / stage;   // two CTAs an SM
     static constexpr int NS = fit > 4 ? 4 : fit < 2 ? 2 : fit;   // stages
-    static constexpr int WK = TM == 16 ? kLoraWarps : 1;  // partial t of a CTA (warps along k)
     static constexpr int LDP = R + 8;                     // floats a row of the partial t
     static constexpr int part_bytes = WK * TM * LDP * 4;
     static constexpr int pool = NS * stage > part_bytes ? NS * stage : part_bytes;
@@ -172,7 +174,8 @@ CQ_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 // Partial t of this CTA: rows [0, TM) of the tile times A over k chunks [ch0, ch1)
 // of KC.  x and A rows come by cp.async through a ring of stages, zero-filled
 // beyond the tile's rows, the rank and K.  TM 64: warp = 16 rows x half the
-// rank; TM 16: warp = one k16 step of each stage, summed at the end.  Leaves the sums
+// rank; TM 16: warp = one k16 step of each stage (rank over 64: and half the rank),
+// summed at the end.  Leaves the sums
 // in part [TM][LDP] (over the ring), after a barrier.
 template <int TM, int R>
 CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_rows,
@@ -206,9 +209,8 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
             }
         }
     };
-    constexpr int WN = TM == 64 ? 2 : 1;
-    constexpr int NT = R / 8 / WN;                // n8 tiles of a warp
-    const int wm = TM == 64 ? warp & 3 : 0, wn = TM == 64 ? warp >> 2 : 0;
+    constexpr int NT = R / 8 / S::WN;             // n8 tiles of a warp
+    const int wm = warp % S::WM, wk = warp / S::WM % S::WK, wn = warp / (S::WM * S::WK);
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; j++)
@@ -239,7 +241,7 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
         if (TM == 16 || 16 * wm < rows) {
 #pragma unroll
             for (int st = 0; st < STEPS; st++) {
-                const uint32_t kb = 32 * (TM == 64 ? st : warp);
+                const uint32_t kb = 32 * (TM == 64 ? st : wk);
                 uint32_t a[4];
                 ldmatrix4(a, base + xa + kb);
 #pragma unroll
@@ -256,7 +258,7 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
     cp_async_wait_group<0>();
     __syncthreads();  // the ring is free
     const int g = lane >> 2, q = lane & 3;
-    float *pw = part + (TM == 64 ? 16 * wm * S::LDP + 8 * NT * wn : warp * TM * S::LDP);
+    float *pw = part + (wk * TM + 16 * wm) * S::LDP + 8 * NT * wn;
 #pragma unroll
     for (int j = 0; j < NT; j++) {
         *reinterpret_cast<float2 *>(pw + g * S::LDP + 8 * j + 2 * q) = make_float2(acc[j][0], acc[j][1]);
@@ -605,7 +607,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     const float fa = s_factor[ra], fb = s_factor[rb];
     int slot = 0;
     for (; nb < nb1; nb += WC) {
-        if (nb + WC < nb1) X::load_b(wn, p, id, rank, (nb + WC) * X::W);
+        // (rank 128: no registers for a second B)
+        if (R <= 64 && nb + WC < nb1) X::load_b(wn, p, id, rank, (nb + WC) * X::W);
         if (rank & 7) X::cut_b(w, rank);
         typename X::Y y;
         cp_async_wait_group<D - 1>();
@@ -613,7 +616,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
         X::run(w, t, y, fa, fb, oa, ob, p.N, nb * X::W);
         request();  // into the slot just taken
         slot = slot + 1 == D ? 0 : slot + 1;
-        w = wn;
+        if (R <= 64)
+            w = wn;
+        else if (nb + WC < nb1)
+            X::load_b(w, p, id, rank, (nb + WC) * X::W);
     }
     cp_async_wait_group<0>();
     __syncwarp();
