@@ -222,7 +222,7 @@ CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_r
     // (a warp with one n8 tile reads it twice)
     const uint32_t wa = (TM + 8 * NT * wn + (lane & 7) + (NT > 1 ? 8 * (lane >> 4) : 0)) * S::pitch +
                         16 * ((lane >> 3) & 1);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < S::NS - 1; i++) {
         if (ch0 + i < ch1) fetch(ch0 + i, i);
         cp_async_commit_group();
@@ -361,11 +361,12 @@ struct Expand {
         uint4 a[2][KS], b[2][KS];  // rows g and g + 8 of lo, hi
     };
     // (hi0, lo0: row g; hi1, lo1: row g + 8)
+    template <bool LO = true>
     CQ_DEV static void load_t(T &o, const __half *hi0, const __half *lo0, const __half *hi1,
                               const __half *lo1) {
         const int q = threadIdx.x & 3;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = LO ? 0 : 1; h < 2; h++) {
             const __half *ta = h ? hi0 : lo0, *tb = h ? hi1 : lo1;
 #pragma unroll
             for (int s = 0; s < KS; s++) {
@@ -461,8 +462,11 @@ struct Expand {
             o.b[i] = src[(2 * i + 1) * kLoraThreads];
         }
     }
+    // LO false: t holds the high parts alone, the low ones are read from lo0 and lo1
+    template <bool LO = true>
     CQ_DEV static void run(const B &w, const T &t, const Y &y, float fa, float fb, float *oa,
-                           float *ob, int N, int n0) {
+                           float *ob, int N, int n0, const __half *lo0 = nullptr,
+                           const __half *lo1 = nullptr) {
         const int c = n0 + 4 * (threadIdx.x & 3);
         float acc[NB][4];
 #pragma unroll
@@ -473,10 +477,18 @@ struct Expand {
         for (int h = 0; h < 2; h++) {  // lo first, then hi
 #pragma unroll
             for (int s = 0; s < KS; s++) {
+                uint4 ta, tb;
+                if (LO || h) {
+                    ta = t.a[h][s];
+                    tb = t.b[h][s];
+                } else {
+                    ta = *reinterpret_cast<const uint4 *>(lo0 + 32 * s + 8 * (threadIdx.x & 3));
+                    tb = *reinterpret_cast<const uint4 *>(lo1 + 32 * s + 8 * (threadIdx.x & 3));
+                }
 #pragma unroll
                 for (int m = 0; m < (R >= 32 ? 2 : 1); m++) {
-                    const uint32_t a[4] = {word(t.a[h][s], 2 * m), word(t.b[h][s], 2 * m),
-                                           word(t.a[h][s], 2 * m + 1), word(t.b[h][s], 2 * m + 1)};
+                    const uint32_t a[4] = {word(ta, 2 * m), word(tb, 2 * m), word(ta, 2 * m + 1),
+                                           word(tb, 2 * m + 1)};
 #pragma unroll
                     for (int j = 0; j < NB; j++)
                         mma_16816(acc[j], a, word(w.w[j][s], 2 * m), word(w.w[j][s], 2 * m + 1));
@@ -603,20 +615,22 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     cluster.barrier_arrive();  // this CTA has read every partial t
 
     typename X::T t;
-    X::load_t(t, th + ra * S::LDT, tl + ra * S::LDT, th + rb * S::LDT, tl + rb * S::LDT);
+    constexpr bool LO = R <= 64;  // (rank 128: the low parts stay in shared memory)
+    const __half *la = tl + ra * S::LDT, *lb = tl + rb * S::LDT;
+    X::template load_t<LO>(t, th + ra * S::LDT, la, th + rb * S::LDT, lb);
     const float fa = s_factor[ra], fb = s_factor[rb];
     int slot = 0;
     for (; nb < nb1; nb += WC) {
-        // (rank 128: no registers for a second B)
-        if (R <= 64 && nb + WC < nb1) X::load_b(wn, p, id, rank, (nb + WC) * X::W);
+        // (rank over 32: no registers for a second B; spilling it cost 4 us at rank 64)
+        if (R <= 32 && nb + WC < nb1) X::load_b(wn, p, id, rank, (nb + WC) * X::W);
         if (rank & 7) X::cut_b(w, rank);
         typename X::Y y;
         cp_async_wait_group<D - 1>();
         X::take_y(y, slots + slot * slot_bytes);
-        X::run(w, t, y, fa, fb, oa, ob, p.N, nb * X::W);
+        X::template run<LO>(w, t, y, fa, fb, oa, ob, p.N, nb * X::W, la, lb);
         request();  // into the slot just taken
         slot = slot + 1 == D ? 0 : slot + 1;
-        if (R <= 64)
+        if (R <= 32)
             w = wn;
         else if (nb + WC < nb1)
             X::load_b(w, p, id, rank, (nb + WC) * X::W);
