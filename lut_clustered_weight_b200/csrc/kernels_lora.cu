@@ -72,9 +72,9 @@ CQ_DEV uint4 keep_first(uint4 v, int k) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One k32 step of the expansion held as 16 bytes per lane and row: lane q of a row's four holds
-// k 8q .. 8q + 7.  MMA step s takes elements 4s .. 4s + 3 as the fragment's k
-// (2q, 2q + 1) and (2q + 8, 2q + 9), for both operands.
+// One k32 step of the expansion held as 16 bytes per lane and row: lane q of a row's
+// four holds k 8q .. 8q + 7.  MMA step s takes elements 4s .. 4s + 3 as the fragment's
+// k (2q, 2q + 1) and (2q + 8, 2q + 9), for both operands.
 CQ_DEV uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // What a CTA of the one-launch form works on.
@@ -175,8 +175,8 @@ CQ_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 // of KC.  x and A rows come by cp.async through a ring of stages, zero-filled
 // beyond the tile's rows, the rank and K.  TM 64: warp = 16 rows x half the
 // rank; TM 16: warp = one k16 step of each stage (rank over 64: and half the rank),
-// summed at the end.  Leaves the sums
-// in part [TM][LDP] (over the ring), after a barrier.
+// summed at the end.  Leaves the sums in part [TM][LDP] (over the ring); a barrier
+// has to follow.
 template <int TM, int R>
 CQ_DEV void shrink(const LoraArgs &p, int id, int rows, int rank, const int *s_rows,
                    unsigned char *ring, float *part, int ch0, int ch1) {
@@ -298,16 +298,18 @@ CQ_DEV void split_row(const float (&v)[(R + 31) / 32], float sc, __half *hi, __h
         const __half h = __float2half_rn(t);
         if (R >= 32 || lane < R) {
             hi[lane + 32 * i] = h;
-            lo[lane + 32 * i] = __float2half_rn(t - __half2float(h));
+            // (a finite t is below 4; an infinite one is hi alone)
+            lo[lane + 32 * i] = __float2half_rn(fabsf(t) <= 4.0f ? t - __half2float(h) : 0.0f);
         }
     }
     if (lane == 0) *factor = sc * up;
 }
 
-// t of the whole cluster, a warp per row, as hi + lo and the factor of the row.
+// t of the whole cluster, a warp per row, as hi + lo and the factor of the row.  Beyond
+// the rank it is 0 (the partial sums there are x times 0: NaN if x is infinite).
 template <int TM, int R>
-CQ_DEV void gather_t(cg::cluster_group &cluster, float *part, int C, int rows, float sc, __half *th,
-                     __half *tl, float *s_factor) {
+CQ_DEV void gather_t(cg::cluster_group &cluster, float *part, int C, int rows, int rank, float sc,
+                     __half *th, __half *tl, float *s_factor) {
     using S = LoraShape<TM, R>;
     constexpr int PER = (R + 31) / 32;
     constexpr int RB = TM == 16 ? 2 : PER > 2 ? 4 : 8;  // rows a warp has in flight
@@ -329,7 +331,7 @@ CQ_DEV void gather_t(cg::cluster_group &cluster, float *part, int C, int rows, f
                     for (int b = 0; b < RB; b++)
 #pragma unroll
                         for (int i = 0; i < PER; i++)
-                            u[k][b][i] = R >= 32 || lane < R
+                            u[k][b][i] = lane + 32 * i < rank
                                              ? rp[(r0 + b * kLoraWarps) * S::LDP + lane + 32 * i]
                                              : 0.0f;
                 }
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
     typename X::B w, wn;
     if (nb < nb1) X::load_b(w, p, id, rank, nb * X::W);
     cluster.sync();
-    gather_t<TM, R>(cluster, part, C, rows, sc, th, tl, s_factor);
+    gather_t<TM, R>(cluster, part, C, rows, rank, sc, th, tl, s_factor);
     __syncthreads();
     cluster.barrier_arrive();  // this CTA has read every partial t
 
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_t(const LoraArgs p) {
                 const int row = r0 + b * C * kLoraWarps;
 #pragma unroll
                 for (int i = 0; i < PER; i++)
-                    u[k][b][i] = row < T.rows && (R >= 32 || lane < R)
+                    u[k][b][i] = row < T.rows && lane + 32 * i < rank
                                      ? rp[row * S::LDP + lane + 32 * i]
                                      : 0.0f;
             }

@@ -339,6 +339,34 @@ def test_lora_add_large_and_tiny_values(cq):
         _lora_check(_lora_run(cq, d), d)
 
 
+@pytest.mark.parametrize("r", [8, 32, 64, 128])
+@pytest.mark.parametrize("M", [40, 600, 2100])
+def test_lora_add_infinite_and_nan_rows(cq, M, r):
+    """An infinite x gives what the sums give, at rank 1 an infinity; a NaN stays in
+    its row; adapters' unused parts hold NaN."""
+    d = _lora_inputs(M, 256, 64, 3, r, np.arange(M) % 3 - 1, seed=M + r)
+    d["ranks"] = np.array([1, r - 3, r], np.int32)
+    d["a"][0, 1:], d["b"][0, :, 1:] = np.nan, np.nan
+    d["a"][1, r - 3:], d["b"][1, :, r - 3:] = np.nan, np.nan
+    bad = [1, 2, 4, M - 2, M - 1]
+    for i, v in zip(bad, (np.inf, np.nan, -np.inf, np.inf, -np.inf)):
+        d["x"][i, 17 + i % 7] = v
+    got = _lora_run(cq, d)
+    ok = np.setdiff1d(np.arange(M), bad)
+    _lora_check(got[torch.from_numpy(ok).to(DEV)], dict(d, x=d["x"][ok], ids=d["ids"][ok], y=d["y"][ok]))
+    for m in bad:
+        i = d["ids"][m]
+        want = d["y"][m].astype(np.float64)
+        if i >= 0:
+            k = d["ranks"][i]
+            with np.errstate(invalid="ignore"):
+                t = d["a"][i, :k].astype(np.float64) @ d["x"][m].astype(np.float64)
+                want = want + float(d["scale"][i]) * (d["b"][i, :, :k].astype(np.float64) @ t)
+            if k == 1 and not np.isnan(d["x"][m]).any():
+                assert np.isinf(want).all()
+        np.testing.assert_array_equal(got[m].cpu().numpy(), want.astype(np.float32))
+
+
 def test_lora_add_refusals(cq):
     d = {k: _dev(v) for k, v in _lora_inputs(4, 64, 32, 2, 8, [0, 1, 0, 1], seed=0).items()}
     ok = lambda **kw: cq.cq_lora_add(*[kw.get(k, d[k]) for k in ("x", "ids", "a", "b", "y")])  # noqa: E731
