@@ -27,7 +27,7 @@ struct NormArgs {
     uint8_t *q;
     float *s;
     int64_t ldq, T;
-    double eps, resid_scale, block_scale, inv_h, sqrt_b;
+    double eps, resid_scale, block_scale, h, inv_h, sqrt_b;
     int H, layer, post_norm, gate_mode, bits, log2b;
     int tpr, rpc;  // threads per row (a multiple of 32), rows per CTA
 };
@@ -95,7 +95,9 @@ CQ_DEV void norm_regs(double (&v)[E], int nv, const NormArgs &a, const __half *w
             t += v[i];
             u += v[i + 1];
         }
-        const double mean = row_sum(t + u, rt) * a.inv_h;
+        // (corrected once: a row of one value has that mean exactly, and 0 is normed)
+        const double sum = row_sum(t + u, rt), m0 = sum * a.inv_h;
+        const double mean = fma(fma(-m0, a.h, sum), a.inv_h, m0);
 #pragma unroll
         for (int c = 0; c < E; c += 8)
             if (c < nv) {
@@ -567,7 +569,8 @@ extern "C" CQ_API cq_status cq_residual_norm(const cq_norm_desc *d, int64_t T, c
     a.s = s_out;
     a.H = (int)d->H;
     a.ldq = d->H * d->act_bits / 8;
-    a.inv_h = 1.0 / (double)d->H;
+    a.h = (double)d->H;
+    a.inv_h = 1.0 / a.h;
     a.eps = d->eps;
     a.resid_scale = d->resid_scale;
     a.block_scale = d->block_scale;

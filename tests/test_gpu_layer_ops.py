@@ -108,6 +108,13 @@ NORM_CASES = [
     (400, 8192, "rms", 32, True, True, "channel", 1.0, 1.0, 4096, 8),
     (320, 2304, "layer", 16, True, False, "none", 1.0, 1.0, 256, 8),
     (310, 16384, "rms", 16, True, False, "none", 1.0, 1.0, 16, 4),
+    (310, 512, "layer", 16, True, False, "element", 1.0, 1.0, 0, 0),
+    (304, 2048, "rms", 32, True, False, "none", 0.5, 1.0, 0, 0),
+    (305, 2048, "rms", 16, True, False, "channel", 1.0, 1.0, 0, 0),
+    (170, 5120, "rms", 32, True, False, "token", 1.0, 1.0, 1024, 8),
+    (160, 5120, "rms", 16, True, True, "none", 1.0, 1.0, 512, 4),
+    (159, 7168, "layer", 32, True, True, "element", 1.0, 1.0, 1024, 4),
+    (150, 8192, "layer", 16, True, False, "none", 1.0, 1.0, 0, 0),
     # the last thread of a row has 8 channels less
     (3, 8200, "rms", 16, True, True, "element", 1.0, 1.0, 8, 4),
     (300, 8216, "layer", 32, True, False, "none", 1.0, 1.0, 4, 8),
@@ -122,8 +129,10 @@ def test_residual_norm_is_the_rounded_definition(cq, T, H, kind, rb, block, post
                                                  had, bits):
     """r' and x bit for bit.  Kernel and reference both work in fp64: they differ
     by about 1e-15 of a value (1e-12 at the worst order of 16384 additions), so
-    the chance that a rounding border of fp16 (2^-11 apart) lies between them is
-    below 1e-8 per value, and the inputs are fixed."""
+    the chance that a rounding border (2^-11 apart in fp16, 2^-24 in fp32) lies
+    between them is below 1e-7 per value, and the inputs are fixed.  A value that
+    the formula puts on a border (a constant row, whose LayerNorm is the bias) has
+    to be formed without any difference."""
     d = _norm_inputs(T, H, kind, rb, block, post, gate, seed=T + H)
     got = _norm_run(cq, d, kind, rs, bs, had, bits)
     torch.cuda.synchronize()
