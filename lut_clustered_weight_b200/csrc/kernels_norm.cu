@@ -294,8 +294,8 @@ CQ_DEV uint32_t nibbles(uint32_t a) {
 // come first and the second, [log2 E, ..), last, so the codes are made in one of
 // few layouts; they go through shared memory once, as bytes, back to the layout
 // of the loads.
-template <int E, bool R16, bool CODES>
-__global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(const NormArgs a) {
+template <int E, int REGS, bool R16, bool CODES>
+__global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
     extern __shared__ __align__(16) double xch_all[];
     __shared__ double red[64];
     __shared__ int s_hi[16];
@@ -485,31 +485,43 @@ __global__ void __maxnreg__(E == 8 ? 64 : E == 16 ? 80 : 128) k_residual_norm(co
     }
 }
 
-template <int E>
+template <int E, int REGS>
 static cudaError_t launch_rows(NormArgs a, bool r16, cudaStream_t st) {
     const int T = (a.H + E - 1) / E;
     a.tpr = (T + 31) / 32 * 32;
     // short rows share a CTA of up to 256 threads
-    a.rpc = (int)std::min<int64_t>(std::max(1, 256 / a.tpr), a.T);
+    a.rpc = (int)std::min<int64_t>(std::max(1, 128 / a.tpr), a.T);
     const bool codes = a.bits > 0;
     const size_t smem = codes ? (size_t)a.rpc * (a.H + a.H / E) * sizeof(double) : 0;
-    auto kern = r16 ? (codes ? k_residual_norm<E, true, true> : k_residual_norm<E, true, false>)
-                    : (codes ? k_residual_norm<E, false, true> : k_residual_norm<E, false, false>);
+    auto kern = r16 ? (codes ? k_residual_norm<E, REGS, true, true> : k_residual_norm<E, REGS, true, false>)
+                    : (codes ? k_residual_norm<E, REGS, false, true>
+                             : k_residual_norm<E, REGS, false, false>);
     count_launch();
     return launch_pdl(kern, dim3((unsigned)((a.T + a.rpc - 1) / a.rpc)), dim3(a.tpr * a.rpc), smem,
                       st, 1, a);
 }
 
-// 16 channels a thread at 80 registers (more registers, fewer rows at once; 64
-// would spill).  Few rows are paced by the length of a row's instruction stream:
-// 8 channels a thread then.  Rows over 8192 take 32, for blocks of at most 512
-// threads.  4096 rows of 2048, codes: 37.5 us with 16, 41.7 with 8; one row of
-// 2560: 4.7 and 3.9.
+// Channels and registers a thread.  16 at 80 registers with codes: fewer channels
+// are more exchanges, and more registers fewer rows at once (4096 rows of 2048: 33.4 us,
+// 8 channels 41.7).  Else:
+//  - rows over 6400 would be alone on their SM at 80 registers, and over 8192 need 64
+//    anyway: 64, some of them spilled (2000 rows of 8192: 93 -> 70 us with codes,
+//    60 -> 48 without; from 4096 up, 3 rows instead of 2: 2000 of 5120, codes 48.5 -> 43.9,
+//    but with a post norm, which spills more, 61 -> 67).  One row an SM or less gains
+//    nothing from room for a second (100 rows of 8192, codes: 7.4 and 7.8).
+//  - few rows are paced by the length of a row's instruction stream: 8 channels (one row
+//    of 2560: 3.7 us, and 4.7 with 16).
+//  - without codes 8 channels, where a thread's fp32 pieces then are 32 bytes apart and not
+//    64 (4096 rows of 2048, fp32 residual: 25.6 us, and 31.3 with 16; fp16, 1024: 10.3 and
+//    10.9), but 16 for long rows of much arithmetic (fp16, 2048: 21.0 and 20.0).
 static cudaError_t launch_residual_norm(const NormArgs &a, bool r16, cudaStream_t st) {
     TimedScope ts(st, CQ_KERNEL_RESIDUAL_NORM);
-    if (a.H > 8192) return launch_rows<32>(a, r16, st);
-    if (a.H <= 4096 && a.T <= 2 * sm_count()) return launch_rows<8>(a, r16, st);
-    return launch_rows<16>(a, r16, st);
+    const bool codes = a.bits > 0, many = a.T > sm_count();
+    if (a.H > 8192 || (many && (a.H > 6400 || (a.H > 4096 && codes && !a.post_norm))))
+        return launch_rows<16, 64>(a, r16, st);
+    if (a.H <= 4096 && (a.T <= 2 * sm_count() || (!codes && (a.H < 2048 || (!r16 && !a.post_norm)))))
+        return launch_rows<8, 64>(a, r16, st);
+    return launch_rows<16, 80>(a, r16, st);
 }
 
 static bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
