@@ -2,20 +2,22 @@
 // and the k / v rows of a cache, from the fp32 rows of a fused QKV projection,
 // sm_100a.
 //
-// A head is head_dim / 8 units of 8 channels; a group of G lanes (a power of
-// two, so that the norm's sum is a shuffle reduction) holds one head, one unit
-// per lane.  A turned unit holds 4 whole pairs, so nothing crosses lanes
-// but the sum: channels [4u, 4u+4) and rot/2 + [4u, 4u+4) (half layout), or
-// [8u, 8u+8) (interleaved).  The angles of a token are formed once per CTA, in
-// fp64: at position 10^6 an fp32 product is off by 0.06 rad.
+// A head is head_dim / 8 units of 8 channels, one unit a thread and round; with a norm
+// a head's units are in a group of G lanes (a power of two, so that the sum is a
+// shuffle reduction), else the units of all heads follow one another.  A turned
+// unit holds 4 whole pairs, so nothing crosses lanes but the sum: channels [4u, 4u+4)
+// and rot/2 + [4u, 4u+4) (half layout), or [8u, 8u+8) (interleaved).  The angles of a
+// token are formed once per CTA, in fp64: at position 10^6 an fp32 product is off by
+// 0.06 rad.
 #include <cmath>
+#include <type_traits>
 
 #include "cq_common.cuh"
 #include "cq_internal.h"
 
 namespace cq {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;  // at most
 constexpr int kRopeMaxDim = 256;
 
 struct RopeArgs {
@@ -26,8 +28,9 @@ struct RopeArgs {
     __half *q, *k, *v;
     const int64_t *slots;
     int64_t tok_stride, head_stride, n_slots;
-    int n_q, n_kv, D, rot, interleaved;
-    int log2g;           // lanes per head: 2^log2g >= D / 8
+    int n_q, n_kv, D, rot;
+    int width, log2w;    // threads per head: D / 8, or G = 2^log2w
+    int step_h, step_u;  // the block's threads are step_h heads and step_u units
     int heads_per_cta;   // heads of a token per CTA (blockIdx.y: which of them)
     float attn_scale, eps;
 };
@@ -37,21 +40,23 @@ CQ_DEV uint32_t pack_half2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// What one lane does in a round: its unit of head h.
+// What one thread does in a round: a unit of head h.
 struct RopeUnit {
-    int h, c0, c1;  // head, first channel of the unit's two halves
+    int h, u, c0, c1;  // head, unit, first channel of the unit's two halves
     bool live, turned, is_v;
     float4 a, b;
 };
 
-CQ_DEV void load_unit(RopeUnit &u, const RopeArgs &p, const float *row, int h, int h_end, int lane) {
+template <bool INTER>
+CQ_DEV void load_unit(RopeUnit &u, const RopeArgs &p, const float *row, int h, int h_end, int unit) {
     u.h = h;
-    u.live = h < h_end && lane < (p.D >> 3);
+    u.u = unit;
+    u.live = h < h_end && unit < (p.D >> 3);
     u.is_v = h >= p.n_q + p.n_kv;
-    u.turned = !u.is_v && lane < (p.rot >> 3);
-    const bool apart = u.turned && !p.interleaved;
-    u.c0 = apart ? 4 * lane : 8 * lane;
-    u.c1 = apart ? (p.rot >> 1) + 4 * lane : u.c0 + 4;
+    u.turned = !u.is_v && unit < (p.rot >> 3);
+    const bool apart = u.turned && !INTER;
+    u.c0 = apart ? 4 * unit : 8 * unit;
+    u.c1 = apart ? (p.rot >> 1) + 4 * unit : u.c0 + 4;
     u.a = u.b = make_float4(0.f, 0.f, 0.f, 0.f);
     if (u.live) {
         const float *src = row + h * p.D;
@@ -60,43 +65,57 @@ CQ_DEV void load_unit(RopeUnit &u, const RopeArgs &p, const float *row, int h, i
     }
 }
 
+// Memory-bound where tokens are many: 4096 of 32 + 8 heads of 128 in 28.5 us, 0.82 of a
+// copy's bandwidth (32.6 with the norms, which add shuffles); one token 2 us.  PACKED:
+// the units of all heads follow one another (width D / 8, not a power of two; 4096 tokens
+// of 24 + 8 heads of 80: 16.9 us, and 21.1 in groups of 16 lanes).  The layout and the
+// norm are template parameters: with all of them read at run time it was bound by
+// instructions (29.2 us).
+template <bool NORM, bool INTER, bool PACKED>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
     __shared__ float2 cs[kRopeMaxDim / 2];
     griddep_wait();
     griddep_launch();
     const int64_t m = blockIdx.x;
     const int heads = p.n_q + 2 * p.n_kv;
-    const int G = 1 << p.log2g, lane = threadIdx.x & (G - 1), groups = kRopeThreads >> p.log2g;
-    const int h_end = min(heads, ((int)blockIdx.y + 1) * p.heads_per_cta);
-    int h0 = blockIdx.y * p.heads_per_cta;
-    const int gh = threadIdx.x >> p.log2g;
+    const int h_begin = blockIdx.y * p.heads_per_cta, h_end = min(heads, h_begin + p.heads_per_cta);
     const float *row = p.qkv + m * heads * p.D;
     // the first round's values are on their way while the angles are formed, every
     // other round's while the one before is worked on
+    const int h_in = PACKED ? threadIdx.x / p.width : threadIdx.x >> p.log2w;
+    int nh = h_begin + h_in, nu = threadIdx.x - (PACKED ? h_in * p.width : h_in << p.log2w);
     RopeUnit next;
-    load_unit(next, p, row, h0 + gh, h_end, lane);
+    load_unit<INTER>(next, p, row, nh, h_end, nu);
     const int64_t slot = p.slots ? p.slots[m] : m;
     const bool cached = !p.slots || (slot >= 0 && slot < p.n_slots);
-    if (threadIdx.x < (p.rot >> 1)) {
+    for (int i = threadIdx.x; i < (p.rot >> 1); i += blockDim.x) {
         // in turns, so that the reduction is a subtraction of the nearest whole one
-        const double turns =
-            (double)p.positions[m] * (double)p.inv_freq[threadIdx.x] * 0.15915494309189535;
+        const double turns = (double)p.positions[m] * (double)p.inv_freq[i] * 0.15915494309189535;
         float s, c;
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-        cs[threadIdx.x] = make_float2(c * p.attn_scale, s * p.attn_scale);
+        cs[i] = make_float2(c * p.attn_scale, s * p.attn_scale);
     }
     __syncthreads();
-    // every lane of a warp runs the same rounds (the shuffles need all of them)
-    for (; h0 < h_end; h0 += groups) {
+    // every thread runs the same rounds (the shuffles need all lanes); h0: the head of
+    // the round's first unit or one before it
+    for (int h0 = h_begin; h0 < h_end; h0 += p.step_h) {
         const RopeUnit u = next;
-        if (h0 + groups < h_end) load_unit(next, p, row, h0 + groups + gh, h_end, lane);
+        nh += p.step_h;
+        if (PACKED) {
+            nu += p.step_u;
+            if (nu >= p.width) {
+                nu -= p.width;
+                nh++;
+            }
+        }
+        if (h0 + p.step_h < h_end) load_unit<INTER>(next, p, row, nh, h_end, nu);
         float v[8] = {u.a.x, u.a.y, u.a.z, u.a.w, u.b.x, u.b.y, u.b.z, u.b.w};
         const __half *w = u.is_v ? nullptr : u.h < p.n_q ? p.qw : p.kw;
-        if (p.qw || p.kw) {
+        if (NORM) {
             float ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; i++) ss += v[i] * v[i];
-            for (int o = G >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int o = p.width >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             if (w && u.live) {
                 const float inv = 1.0f / sqrtf(ss / (float)p.D + p.eps);
                 const uint2 w0 = *reinterpret_cast<const uint2 *>(w + u.c0);
@@ -114,8 +133,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
         if (u.turned) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const float2 t = cs[4 * lane + i];
-                if (p.interleaved) {
+                const float2 t = cs[4 * u.u + i];
+                if (INTER) {
                     const float a = v[2 * i], b = v[2 * i + 1];
                     v[2 * i] = a * t.x - b * t.y;
                     v[2 * i + 1] = a * t.y + b * t.x;
@@ -194,22 +213,34 @@ extern "C" CQ_API cq_status cq_rope_qkv(const cq_rope_desc *d, int64_t M, const 
     p.n_kv = (int)d->n_kv;
     p.D = (int)d->head_dim;
     p.rot = (int)d->rot_dim;
-    p.interleaved = d->interleaved;
     p.attn_scale = d->attn_scale;
     p.eps = d->eps;
-    for (p.log2g = 0; (8 << p.log2g) < p.D; p.log2g++) {
+    const bool norm = p.qw || p.kw;
+    for (p.log2w = 0; (8 << p.log2w) < p.D; p.log2w++) {
     }
-    // one CTA a token (the angles once); few tokens: one round of heads a CTA
-    const int heads = p.n_q + 2 * p.n_kv, groups = kRopeThreads >> p.log2g;
-    const int rounds = (heads + groups - 1) / groups;
+    p.width = norm ? 1 << p.log2w : p.D / 8;
+    const bool packed = p.width != 1 << p.log2w;
+    // One CTA a token (the angles once), of no more threads than its rounds need (20 heads
+    // of 64 and 4096 tokens: 8.2 us with 192, 10.2 with 256); few tokens: one round of
+    // whole heads a CTA.
+    const int heads = p.n_q + 2 * p.n_kv, units = heads * p.width;
+    const int rounds = (units + kRopeThreads - 1) / kRopeThreads;
+    const int threads = ((units + rounds - 1) / rounds + 31) / 32 * 32;
     const bool split = M * rounds <= 4LL * sm_count();
-    p.heads_per_cta = split ? groups : heads;
+    p.step_h = threads / p.width;
+    p.step_u = threads % p.width;
+    p.heads_per_cta = split ? p.step_h : heads;
+    const unsigned parts = (heads + p.heads_per_cta - 1) / p.heads_per_cta;
+    auto pick = [&](auto inter) {
+        constexpr bool I = decltype(inter)::value;
+        return norm ? k_rope_qkv<true, I, false> : packed ? k_rope_qkv<false, I, true> : k_rope_qkv<false, I, false>;
+    };
     try {
         cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
         TimedScope ts(st, CQ_KERNEL_ROPE_QKV);
         count_launch();
-        return launch_pdl(k_rope_qkv, dim3((unsigned)M, split ? rounds : 1), dim3(kRopeThreads), 0, st, 1, p) ==
-                       cudaSuccess
+        auto kern = d->interleaved ? pick(std::true_type{}) : pick(std::false_type{});
+        return launch_pdl(kern, dim3((unsigned)M, parts), dim3(threads), 0, st, 1, p) == cudaSuccess
                    ? CQ_OK
                    : CQ_ERR_CUDA;
     } catch (...) {

@@ -404,6 +404,12 @@ ROPE_CASES = [
     (11, 5, 5, 192, 0, False, "qk", 8, 1.0, "rows"),
     (2, 300, 10, 16, 8, False, "", 8, 0.5, None),
     (1021, 8, 2, 64, 32, False, "qk", 1 << 20, 1.0, "rows"),
+    # heads whose units are not a power of two, in several rounds of one CTA
+    (600, 30, 5, 80, 40, False, "", 32768, 1.0, "rows"),
+    (601, 9, 3, 248, 248, True, "", 32768, 1.0, "heads"),
+    (613, 6, 2, 24, 24, False, "", 32768, 0.7, None),
+    (640, 16, 4, 64, 64, False, "", 32768, 1.0, "rows"),      # fewer threads than 256
+    (602, 25, 2, 120, 64, False, "k", 32768, 1.0, "rows"),
 ]
 
 
