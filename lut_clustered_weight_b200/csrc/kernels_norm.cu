@@ -30,6 +30,7 @@ struct NormArgs {
     double eps, resid_scale, block_scale, h, inv_h, sqrt_b;
     int H, layer, post_norm, gate_mode, bits, log2b;
     int tpr, rpc;  // threads per row (a multiple of 32), rows per CTA
+    int64_t ahead; // rows from a row to the one that takes its place on the SM
 };
 
 // Threads of a row.  Sums go through shared memory; the half of the
@@ -294,6 +295,12 @@ CQ_DEV uint32_t nibbles(uint32_t a) {
 // come first and the second, [log2 E, ..), last, so the codes are made in one of
 // few layouts; they go through shared memory once, as bytes, back to the layout
 // of the loads.
+// A later row's bytes, into the L2
+CQ_DEV void prefetch_row(const void *p, int bytes, int j, int threads) {
+    for (int i = 128 * j; i < bytes; i += 128 * threads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p) + i));
+}
+
 template <int E, int REGS, bool R16, bool CODES>
 __global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
     extern __shared__ __align__(16) double xch_all[];
@@ -323,6 +330,12 @@ __global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
     const int nv = t < a.T ? max(0, min(E, H - c0)) : 0;  // a multiple of 8
     const int64_t at = t * H + c0;
 
+    if (!CODES && t + a.ahead < a.T) {
+        const int64_t next = (t + a.ahead) * H;
+        prefetch_row(reinterpret_cast<const char *>(a.resid) + next * (R16 ? 2 : 4), H * (R16 ? 2 : 4), rt.j, a.tpr);
+        if (a.y) prefetch_row(a.y + next, H * 4, rt.j, a.tpr);
+        if (a.gate_mode == CQ_GATE_ELEMENT) prefetch_row(a.gate + next, H * 2, rt.j, a.tpr);
+    }
     double v[E];
     // everything the row reads once is requested before the first use
     uint4 rr[RS];
@@ -492,6 +505,11 @@ static cudaError_t launch_rows(NormArgs a, bool r16, cudaStream_t st) {
     // short rows share a CTA of up to 256 threads
     a.rpc = (int)std::min<int64_t>(std::max(1, 128 / a.tpr), a.T);
     const bool codes = a.bits > 0;
+    // A row fetches the one that takes its place where the arithmetic is short (4096 rows of
+    // 2048, fp32 residual: 25.5 -> 22.8 us); with codes or a second norm that only adds
+    // instructions (codes 33.6 -> 34.0).
+    const int ctas = std::max(1, std::min(32, 65536 / (REGS * a.tpr * a.rpc)));
+    a.ahead = codes || a.post_norm ? a.T : (int64_t)ctas * a.rpc * sm_count();
     const size_t smem = codes ? (size_t)a.rpc * (a.H + a.H / E) * sizeof(double) : 0;
     auto kern = r16 ? (codes ? k_residual_norm<E, REGS, true, true> : k_residual_norm<E, REGS, true, false>)
                     : (codes ? k_residual_norm<E, REGS, false, true>
@@ -513,7 +531,8 @@ static cudaError_t launch_rows(NormArgs a, bool r16, cudaStream_t st) {
 //    of 2560: 3.7 us, and 4.7 with 16).
 //  - without codes 8 channels, where a thread's fp32 pieces then are 32 bytes apart and not
 //    64 (4096 rows of 2048, fp32 residual: 25.6 us, and 31.3 with 16; fp16, 1024: 10.3 and
-//    10.9), but 16 for long rows of much arithmetic (fp16, 2048: 21.0 and 20.0).
+//    10.9; all before rows were fetched ahead), but 16 for long rows of much arithmetic
+//    (fp16, 2048: 21.0 and 20.0).
 static cudaError_t launch_residual_norm(const NormArgs &a, bool r16, cudaStream_t st) {
     TimedScope ts(st, CQ_KERNEL_RESIDUAL_NORM);
     const bool codes = a.bits > 0, many = a.T > sm_count();
