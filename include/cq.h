@@ -432,7 +432,8 @@ CQ_API cq_status cq_lora_add(const void *x, const int32_t *ids, int64_t M, int64
  *            tokens have the same slot, its contents are unspecified.
  * Requires head_dim % 8 == 0, 8 <= head_dim <= 256, rot_dim % 8 == 0,
  * 0 <= rot_dim <= head_dim, n_q >= 1, n_kv >= 1, n_q + 2 n_kv <= 1024, strides
- * multiples of 8 and >= 0, M <= 2^31 - 1 (M = 0 is a no-op), eps > 0.
+ * multiples of 8, >= 0, and >= head_dim where more than one head (n_kv > 1) or
+ * token (M > 1) is written, M <= 2^31 - 1 (M = 0 is a no-op), eps > 0.
  */
 typedef struct {
     int64_t n_q, n_kv, head_dim, rot_dim;

@@ -196,6 +196,10 @@ extern "C" CQ_API cq_status cq_rope_qkv(const cq_rope_desc *d, int64_t M, const 
         d->kv_token_stride % 8 || d->kv_head_stride % 8 || M > INT32_MAX)
         return CQ_ERR_UNSUPPORTED;
     if (M == 0) return CQ_OK;
+    // heads or rows of the cache on top of one another
+    if ((d->n_kv > 1 && d->kv_head_stride < d->head_dim) ||
+        (M > 1 && d->kv_token_stride < d->head_dim))
+        return CQ_ERR_INVALID_ARGUMENT;
     RopeArgs p{};
     p.qkv = qkv;
     p.positions = positions;

@@ -172,6 +172,12 @@ def test_rope_qkv_argument_checks():
     assert f(M=0, rot_dim=0, freq=None, slots=FAKE) == OK
 
 
+def test_rope_qkv_refuses_cache_rows_on_top_of_one_another():
+    for kw in (dict(kv_head_stride=0), dict(kv_head_stride=56), dict(kv_token_stride=0),
+               dict(kv_token_stride=56), dict(kv_token_stride=0, slots=FAKE)):
+        assert _rope_call(**kw) == BAD, kw
+
+
 # ---------------------------------------------------------------- the binding's checks
 
 
