@@ -149,7 +149,9 @@ struct LoraShape {
     static constexpr int WM = TM / 16;                    // warps along the rows
     static constexpr int WN = TM == 64 || R == 128 ? 2 : 1;  // along the rank
     static constexpr int WK = kLoraWarps / WM / WN;       // along k: partial t of a CTA
-    static constexpr int KC = TM == 64 ? 64 : 16 * WK;    // k of a stage
+    // k of a stage (TM 64: fewer, longer stages where the rank is large: 2442 rows, K 6448, rank
+    // 64 46.5 us, and 48.3 with 64; rank 16 27.8, and 23.2)
+    static constexpr int KC = TM == 64 ? (R >= 64 ? 128 : 64) : 16 * WK;
     static constexpr int pitch = 2 * KC + 16;             // bytes of a staged row (ldmatrix: no conflicts)
     static constexpr int rows = TM + R;                   // x rows, then A rows
     static constexpr int stage = rows * pitch;
