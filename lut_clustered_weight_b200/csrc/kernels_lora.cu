@@ -35,9 +35,10 @@ namespace cq {
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraMaxRank = 128;
-// Up to this many rows (one a thread) every CTA finds its own tile in the ids;
-// above, one CTA sorts the rows first (k_lora_plan).
-constexpr int kLoraSmallM = kLoraThreads;
+// One launch in which every CTA finds its own tile in the ids: always up to kLoraOneM
+// rows, by the work up to one row a thread (lora_one_launch).  Else one CTA sorts the rows
+// first (k_lora_plan).
+constexpr int kLoraOneM = 40;
 
 struct LoraTile {
     int id, start, rows, rank;  // id -1: no adapter; start: of its rows among the sorted ones
@@ -53,7 +54,7 @@ struct LoraArgs {
     float *out;
     int64_t ldy, ldo;
     int M, K, N, n, r;
-    // planned launches only (M > kLoraSmallM)
+    // planned launches only
     const int *n_tiles;
     const LoraTile *tiles;
     const int *list;  // rows of tile i at list[i * TM ..)
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora(const LoraArgs p) {
 }
 
 // ---------------------------------------------------------------- many rows
-// Above kLoraSmallM rows the two products are launches of their own: a tile's
+// Where rows or work are many the two products are launches of their own: a tile's
 // shrink is short and waits on latencies, its expansion streams y, and in one
 // launch all CTAs would be in the same phase at the same time (4096 rows, K 2048,
 // N 2816, rank 64: 20 of 45 us with y on its way).
@@ -988,6 +989,17 @@ static int64_t lora_max_tiles(int64_t M, int64_t n) {
     return M / lora_tile_rows(M) + std::min(n + 1, M);
 }
 static int lora_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+// The one-launch form has no sort before it (3 us) but does all of a tile in one cluster:
+// it is behind where tiles are many waves of clusters or long.  Measured, us, one launch
+// and planned: 64 rows, K = N = 4096, 32 adapters of rank 64: 14.0 and 15.8, 64 adapters:
+// 27.1 and 23.8; 192 rows, 32 adapters: 19.0 and 17.3; 192 rows, K = N = 2048, 8 adapters
+// of rank 64: 12.4 and 11.3, at K = N = 512: 7.3 and 9.9; 128 rows over 200 adapters of
+// rank 16, K 2560, N 6144: 34 and 27.
+static bool lora_one_launch(int64_t M, int64_t K, int64_t N, int64_t n, int64_t r) {
+    if (M <= kLoraOneM || M > kLoraThreads) return M <= kLoraOneM;
+    const int64_t tiles = lora_max_tiles(M, n), work = tiles * 16 * lora_rank(r) * (K + N);
+    return work < 48000000 || (M <= 160 && tiles <= 80 && work < 350000000);
+}
 // Scratch of a planned call: tile count, tiles, their rows, places, t, factors.
 struct LoraScratch {
     size_t tiles, list, place, t, factor, total;
@@ -1036,7 +1048,7 @@ static cudaError_t launch_planned(LoraArgs p, cudaStream_t st) {
 static cudaError_t launch_lora(LoraArgs p, void *ws, cudaStream_t st) {
     TimedScope ts(st, CQ_KERNEL_LORA_ADD);
     const int R = lora_rank(p.r);
-    if (p.M <= kLoraSmallM)
+    if (lora_one_launch(p.M, p.K, p.N, p.n, p.r))
         return R == 16   ? launch_small<16>(p, st)
                : R == 32 ? launch_small<32>(p, st)
                : R == 64 ? launch_small<64>(p, st)
@@ -1074,7 +1086,7 @@ extern "C" {
 
 CQ_API size_t cq_lora_add_workspace_size(int64_t M, int64_t n_adapters, int64_t r_max) {
     using namespace cq;
-    if (M <= kLoraSmallM || M > (int64_t(1) << 24) || n_adapters <= 0 || n_adapters > 4096 ||
+    if (M <= kLoraOneM || M > (int64_t(1) << 24) || n_adapters <= 0 || n_adapters > 4096 ||
         r_max <= 0 || r_max > kLoraMaxRank)
         return 0;
     return lora_scratch(M, n_adapters, r_max).total;

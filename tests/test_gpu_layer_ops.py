@@ -273,6 +273,13 @@ LORA_CASES = [
     (300, 8192, 2056, 2, 128, "runs", False),
     (5, 8192, 4104, 2, 16, "rows", False),
     (5, 8192, 4104, 2, 128, "rows", False),
+    # up to 256 rows in either form, by the work
+    (41, 4096, 4104, 60, 64, "each", True),
+    (100, 1024, 1032, 200, 16, "rows", False),
+    (161, 2048, 1032, 40, 32, "runs", True),
+    (161, 136, 136, 40, 32, "runs", True),
+    (256, 2560, 264, 3, 128, "rows", True),
+    (200, 1024, 1024, 7, 64, "none", False),
     (9000, 16, 24, 5, 8, "rows", False),           # more rows than the sorting CTA holds
     (17000, 8, 8, 1100, 8, "rows", True),
 ]
