@@ -39,7 +39,8 @@
  *               but outside what the kernels handle), or CQ_ERR_WORKSPACE
  *               (workspace too small) and enqueues nothing.  CQ_ERR_CUDA
  *               reports a launch error.
- *   Inputs      must be finite; NaN / Inf give unspecified outputs.
+ *   Inputs      must be finite; NaN / Inf give unspecified outputs, unless the
+ *               entry point says what they give.
  *   Threads     re-entrant; calls on different streams may run concurrently.
  */
 #ifndef CQ_H_
@@ -339,7 +340,9 @@ CQ_API cq_status cq_moe_ffn(const cq_moe_desc *d, const void *x, const float *ro
  * x_out      fp16 [T, H]
  * q_out, s_out  as cq_rotate_quantize; both NULL iff act_bits = 0
  * The outputs may not overlap each other or any input, resid_out = resid
- * apart.  r' and x must stay inside the range of their type.
+ * apart.  A NaN or an infinity in an operand (and a finite r' or x beyond its
+ * type's range, which is rounded to an infinity) gives in r' and x what the
+ * formula gives; a row whose x holds one gets the scale NaN and codes 0.
  * Requires H % 8 == 0, 8 <= H <= 16384, T <= 2^31 - 1; T >= 0 (T = 0 is a
  * no-op); eps > 0 and finite, scales finite; act_bits in {0, 4, 8}; with
  * codes, had_block as cq_rotate_quantize (0 without).

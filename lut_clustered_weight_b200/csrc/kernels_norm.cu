@@ -59,7 +59,9 @@ CQ_DEV double row_sum(double v, RowThreads &rt) {
 // fp64 is involved: the fp16 bits are put at the top of an fp64 word by two or
 // three integer instructions (sign in place, exponent and mantissa below a
 // field of zeros).  That is the value times 2^-1008, exactly, zeros and
-// subnormals included (they are fp64 subnormals of the same pattern).
+// subnormals included (they are fp64 subnormals of the same pattern).  An infinity
+// comes out as 65536 of its sign, a NaN as more: who uses the values looks for
+// those with OddTest and puts the result right with mend_odd.
 constexpr double kHalfUp = 0x1p1008;
 CQ_DEV double half_tiny(int top) {  // fp16 in the upper half of top
     return __hiloint2double((top >> 6) & 0x81fffc00, 0);
@@ -82,6 +84,39 @@ CQ_DEV void halves(const uint4 &u, double *v) {
         v[2 * i] = (double)f.x;
         v[2 * i + 1] = (double)f.y;
     }
+}
+
+// Whether some fp16 values hold an infinity or a NaN: the product with 0 is NaN then, else
+// 0 (about 5 instructions for 8 values).  Looking costs 1 % with codes (4096 rows of 2048:
+// 33.7 -> 34.0 us) and 3 % where a row has five fp16 operands (LayerNorm twice with a gate,
+// 1021 x 4096: 25.4 -> 26.2).  Without branches, by a NaN in the factor that the values are
+// used with, it costs as much (34.4 and 25.8) and spoils the channels beside them.
+struct OddTest {
+    uint32_t m = 0;
+    CQ_DEV void add(const uint4 &u) {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+        const __half2 z = __float2half2_rn(0.0f);
+        const __half2 p = __hfma2(h[1], z, __hmul2(h[0], z)), q = __hfma2(h[3], z, __hmul2(h[2], z));
+        m |= *reinterpret_cast<const uint32_t *>(&p) | *reinterpret_cast<const uint32_t *>(&q);
+    }
+    CQ_DEV bool odd() const { return __builtin_expect((m & 0x7fff7fffu) != 0, 0); }
+};
+CQ_DEV bool odd_half(unsigned h) { return (h & 0x7c00) == 0x7c00; }
+// The E channels of v have been multiplied by (or, PLUS, had added) what half_tiny made of
+// the fp16 values at p.  What is still to be done where one is not finite: a product with an
+// infinity (its sign is v's already) or a NaN, or an addition of it.  The values are
+// read again, so that the path that all calls take holds nothing for this.
+template <int E, bool PLUS>
+CQ_DEV void mend_odd(double (&v)[E], int nv, const __half *p) {
+#pragma unroll
+    for (int i = 0; i < E; i++)
+        if (i < nv) {
+            const unsigned short h = __half_as_ushort(p[i]);
+            if (odd_half(h)) {
+                const double o = (double)__half2float(__ushort_as_half(PLUS ? h : h & 0x7fff));
+                v[i] = PLUS ? v[i] + o : v[i] * o;
+            }
+        }
 }
 
 // v = norm(v) over the row; nv of the thread's E channels exist, the others are
@@ -119,9 +154,11 @@ CQ_DEV void norm_regs(double (&v)[E], int nv, const NormArgs &a, const __half *w
         u = fma(v[i + 1], v[i + 1], u);
     }
     const double inv = rsqrt(fma(row_sum(t + u, rt), a.inv_h, a.eps));
+    OddTest odd;
 #pragma unroll
     for (int c = 0; c < E; c += 8) {
         if (w) {
+            odd.add(wv[c / 8]);
             double f[8];
             halves_tiny(wv[c / 8], f);
 #pragma unroll
@@ -130,13 +167,22 @@ CQ_DEV void norm_regs(double (&v)[E], int nv, const NormArgs &a, const __half *w
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c + i] *= inv;
         }
-        if (b && c < nv) {
+    }
+    if (odd.odd()) mend_odd<E, false>(v, nv, w + c0);
+    if (!b) return;
+    odd = OddTest{};
+#pragma unroll
+    for (int c = 0; c < E; c += 8) {
+        if (c < nv) {
+            const uint4 bv = *reinterpret_cast<const uint4 *>(b + c0 + c);
+            odd.add(bv);
             double f[8];
-            halves_tiny(*reinterpret_cast<const uint4 *>(b + c0 + c), f);
+            halves_tiny(bv, f);
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c + i] = fma(f[i], kHalfUp, v[c + i]);
         }
     }
+    if (odd.odd()) mend_odd<E, true>(v, nv, b + c0);
 }
 
 // Butterfly levels [L0, N) over 2^N registers at v[0 .. 2^N)
@@ -368,15 +414,19 @@ __global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
             for (int i = 0; i < E; i++) v[i] *= g;
         } else if (a.gate_mode != CQ_GATE_NONE) {
             const __half *gp = a.gate + (a.gate_mode == CQ_GATE_CHANNEL ? c0 : at);
+            OddTest odd;
 #pragma unroll
             for (int c = 0; c < E; c += 8) {
                 if (c < nv) {
+                    const uint4 gv = *reinterpret_cast<const uint4 *>(gp + c);
+                    odd.add(gv);
                     double f[8];
-                    halves_tiny(*reinterpret_cast<const uint4 *>(gp + c), f);
+                    halves_tiny(gv, f);
 #pragma unroll
                     for (int i = 0; i < 8; i++) v[c + i] *= f[i] * kHalfUp;
                 }
             }
+            if (odd.odd()) mend_odd<E, false>(v, nv, gp);
         }
     }
     // r' = round(resid_scale * r + block_scale * v)
@@ -414,6 +464,7 @@ __global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
         }
     }
     norm_regs<E>(v, nv, a, a.pre_w, a.pre_b, c0, rt);
+    OddTest odd;
 #pragma unroll
     for (int c = 0; c < E / 8; c++) {
         uint4 o;
@@ -422,9 +473,15 @@ __global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
         for (int i = 0; i < 8; i += 2)
             h[i / 2] = __halves2half2(__double2half(v[8 * c + i]), __double2half(v[8 * c + i + 1]));
         if (8 * c < nv) *reinterpret_cast<uint4 *>(a.x + at + 8 * c) = o;
-        if (CODES) halves_tiny(o, v + 8 * c);
+        if (CODES) {
+            odd.add(o);
+            halves_tiny(o, v + 8 * c);
+        }
     }
     if (!CODES) return;
+    // a row whose x is not finite: the high word of a NaN as its largest magnitude, above
+    // any value's, so its scale is NaN and its codes are 0
+    if (odd.odd()) atomicMax(&s_hi[row], 0x7ff80000);
 
     // ---- rotation (channels beyond the row are zeros of whole blocks of 8)
     const int lb = a.log2b;

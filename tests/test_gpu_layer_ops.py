@@ -202,6 +202,63 @@ def test_residual_norm_empty(cq):
     assert r.shape == x.shape == (0, 64)
 
 
+@pytest.mark.parametrize("T,H,had,bits", [(6, 512, 64, 8), (6, 2048, 2048, 4), (400, 2048, 16, 8),
+                                          (150, 8216, 8, 4), (400, 2048, 0, 0)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["channel", "token", "element"])
+def test_residual_norm_passes_on_what_is_not_finite(cq, T, H, had, bits, kind, gate):
+    """A NaN or an infinity in an operand gives in r' and x what the formula gives.
+    A row whose x holds one has the scale NaN and codes 0; the other rows do not
+    change.  (A finite x beyond fp16 is an infinity like another.)"""
+    clean = _norm_inputs(T, H, kind, 16, True, True, gate, seed=11)
+    # resid and y at (row 1, ..): their row alone; a weight or bias: every row
+    spots = [("resid", 1), ("y", 1), ("gate", 1), ("pre", 0), ("post", 0)]
+    if kind == "layer":
+        spots += [("pre", 1), ("post", 1)]
+    for n, (name, i) in enumerate(spots):
+        for bad in (np.nan, np.inf, -np.inf):
+            d = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in clean.items()}
+            c = (8 * n + 5) % H
+            if name in ("pre", "post"):
+                d[name] = tuple(None if w is None else w.copy() for w in d[name])
+                d[name][i][c] = bad
+            elif d[name].ndim == 1:
+                d[name][c] = bad
+            else:
+                d[name][1, min(c, d[name].shape[1] - 1)] = bad
+            got = _norm_run(cq, d, kind, 1.0, 1.0, had, bits)
+            with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
+                r, x = _norm_ref(d, kind, 1.0, 1.0)
+            np.testing.assert_array_equal(got[0].cpu().numpy(), r)
+            np.testing.assert_array_equal(got[1].cpu().numpy(), x)
+            if bits:
+                ok = np.isfinite(x).all(axis=1)
+                q, s = oracle.unpack_codes(got[2].cpu().numpy(), H, bits), got[3].cpu().numpy()
+                assert not ok.all() and np.isnan(s[~ok]).all() and not q[~ok].any()
+                if ok.any():
+                    qr, sr = oracle.rotate_quantize(np.ascontiguousarray(x[ok]), had, bits)
+                    assert np.array_equal(q[ok], qr) and np.array_equal(s[ok], sr)
+
+
+def test_residual_norm_scale_of_a_row_beyond_fp16(cq):
+    """x overflows fp16 in one channel of a row of finite operands."""
+    T, H = 3, 64
+    d = _norm_inputs(T, H, "rms", 16, False, False, "none", seed=2)
+    w = d["pre"][0]
+    w[:] = 1
+    w[9] = 6e4
+    d["resid"][:] = 1
+    d["resid"][0, 9] = 0
+    d["resid"][1, 9] = 4                                      # 4 / sqrt(79 / 64) * 6e4 > 65504
+    d["resid"][2, 9] = 1 / 64
+    _, x, q, s = _norm_run(cq, d, "rms", 1.0, 1.0, 16, 8)
+    x, q, s = x.cpu().numpy(), q.cpu().numpy(), s.cpu().numpy()
+    assert np.isinf(x[1, 9]) and np.isfinite(x[[0, 2]]).all()
+    assert np.isnan(s[1]) and not q[1].any()
+    qr, sr = oracle.rotate_quantize(np.ascontiguousarray(x[[0, 2]]), 16, 8)
+    assert np.array_equal(q[[0, 2]], qr) and np.array_equal(s[[0, 2]], sr)
+
+
 # ---------------------------------------------------------------- low-rank adapters
 
 
