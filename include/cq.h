@@ -437,6 +437,10 @@ CQ_API cq_status cq_lora_add(const void *x, const int32_t *ids, int64_t M, int64
  * 0 <= rot_dim <= head_dim, n_q >= 1, n_kv >= 1, n_q + 2 n_kv <= 1024, strides
  * multiples of 8, >= 0, and >= head_dim where more than one head (n_kv > 1) or
  * token (M > 1) is written, M <= 2^31 - 1 (M = 0 is a no-op), eps > 0.
+ * No two rows written may share addresses.  Without slots that is checked; with
+ * slots any strides that keep to the above are taken (a cache [sequence, head,
+ * token, channel] has rows of one head between those of another), and
+ * distinct addresses are the caller's part.
  */
 typedef struct {
     int64_t n_q, n_kv, head_dim, rot_dim;

@@ -164,6 +164,20 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
     }
 }
 
+// Whether k rows m tok + h head of D elements, m < M and h < n_kv (both strides at least D),
+// share addresses.  Rows m and m + dm of heads h + dh and h lie |dm tok - dh head| apart,
+// closest at the dm on either side of dh head / tok.
+static bool rows_share(int64_t M, int64_t n_kv, int64_t tok, int64_t head, int64_t D) {
+    if (static_cast<__int128>(n_kv - 1) * head + D <= tok) return false;  // a row's heads side by side
+    for (int64_t dh = 1; dh < n_kv; dh++) {
+        const __int128 off = static_cast<__int128>(dh) * head;
+        const __int128 below = off / tok, left = off - below * tok;
+        if (below >= 1 && below < M && left < D) return true;
+        if (below + 1 < M && tok - left < D) return true;
+    }
+    return false;
+}
+
 static bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace cq
@@ -196,9 +210,13 @@ extern "C" CQ_API cq_status cq_rope_qkv(const cq_rope_desc *d, int64_t M, const 
         d->kv_token_stride % 8 || d->kv_head_stride % 8 || M > INT32_MAX)
         return CQ_ERR_UNSUPPORTED;
     if (M == 0) return CQ_OK;
-    // heads or rows of the cache on top of one another
+    // heads or rows of the cache on top of one another: within a row or a head, and, where
+    // the rows are known (no slots), anywhere
     if ((d->n_kv > 1 && d->kv_head_stride < d->head_dim) ||
         (M > 1 && d->kv_token_stride < d->head_dim))
+        return CQ_ERR_INVALID_ARGUMENT;
+    if (!slots && M > 1 &&
+        rows_share(M, d->n_kv, d->kv_token_stride, d->kv_head_stride, d->head_dim))
         return CQ_ERR_INVALID_ARGUMENT;
     RopeArgs p{};
     p.qkv = qkv;

@@ -561,6 +561,36 @@ def test_rope_qkv_into_a_cache_of_sequences(cq):
     assert torch.equal(q0, q1) and torch.equal(kc, want_k) and torch.equal(vc, want_v)
 
 
+@pytest.mark.parametrize("M,nkv,ts,hs", [
+    (3, 2, 2, 1),      # rows of a token
+    (3, 2, 1, 3),      # heads outermost
+    (3, 2, 5, 2),      # gaps between heads and rows
+    (3, 2, 2, 3),      # neither inside the other, and nothing shared
+    (1, 3, 0, 1),      # one row: its stride does not matter
+    (4, 1, 1, 0),      # one head: the same
+])
+def test_rope_qkv_writes_any_rows_that_share_nothing(cq, M, nkv, ts, hs):
+    """k and v rows without slots, strides in heads of 16 channels."""
+    nq, D = 2, 16
+    g = np.random.default_rng(M + 10 * nkv)
+    qkv = _dev(g.standard_normal((M, (nq + 2 * nkv) * D)).astype(np.float32))
+    pos = _dev(np.arange(M, dtype=np.int32))
+    freq = _dev(cq.rope_inv_freq(D))
+    _, k0, v0 = cq.cq_rope_qkv(qkv, pos, freq, nq, nkv, head_dim=D)
+    n = ((M - 1) * ts + (nkv - 1) * hs + 1) * D
+    bufs = [torch.full((n + 8,), 9.0, dtype=torch.float16, device=DEV) for _ in range(2)]
+    want = [b.clone() for b in bufs]
+    kv = [b[:n].as_strided((M, nkv, D), (ts * D, hs * D, 1)) for b in bufs]
+    cq.cq_rope_qkv(qkv, pos, freq, nq, nkv, head_dim=D, k_out=kv[0], v_out=kv[1])
+    for w, b, ref0 in zip(want, bufs, (k0, v0)):
+        w[:n].as_strided((M, nkv, D), (ts * D, hs * D, 1)).copy_(ref0)
+        assert torch.equal(w, b)
+    if M > 1 and nkv > 1:
+        with pytest.raises(cq.CQError):
+            same = [b[:n].as_strided((M, nkv, D), (D, D, 1)) for b in bufs]
+            cq.cq_rope_qkv(qkv, pos, freq, nq, nkv, head_dim=D, k_out=same[0], v_out=same[1])
+
+
 def test_rope_qkv_refusals(cq):
     qkv = torch.zeros((2, 64), device=DEV)
     pos = torch.zeros(2, dtype=torch.int32, device=DEV)

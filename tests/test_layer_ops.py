@@ -178,6 +178,25 @@ def test_rope_qkv_refuses_cache_rows_on_top_of_one_another():
         assert _rope_call(**kw) == BAD, kw
 
 
+def test_rope_qkv_refuses_heads_of_one_row_on_heads_of_another():
+    """Without slots the rows written are known: strides that put head h of row m and
+    another head of another row at common addresses are refused, each larger than a
+    head though they be."""
+    D = 16
+    for M in (2, 3, 5):
+        for nkv in (2, 3, 4):
+            for ts in range(D, 8 * D, 8):
+                for hs in range(D, 8 * D, 8):
+                    at = sorted(m * ts + h * hs for m in range(M) for h in range(nkv))
+                    if any(b - a < D for a, b in zip(at, at[1:])):
+                        kw = dict(M=M, n_kv=nkv, head_dim=D, rot_dim=D, kv_token_stride=ts,
+                                  kv_head_stride=hs)
+                        assert _rope_call(**kw) == BAD, kw
+    assert _rope_call(kv_token_stride=64) == BAD
+    big = 1 << 62                              # no product of a stride and a count wraps
+    assert _rope_call(M=1 << 20, n_kv=500, kv_token_stride=big, kv_head_stride=big) == BAD
+
+
 # ---------------------------------------------------------------- the binding's checks
 
 
