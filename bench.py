@@ -699,24 +699,13 @@ def measure_codebook_sizes(cq, args, dev, peaks, copies=3):
     return out
 
 
-def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers=4):
-    """Decode step of n_layers Qwen3-4B-shaped decoder layers (hidden 2560, 32
-    query / 8 key-value heads of 128, intermediate 9728, a KV cache of ctx
-    tokens per sequence, M sequences decoding one token each), once with the
-    linears as this library's LUT layers (QKV and O through
-    cq_rotate_quantize + cq_lut_gemm, the SwiGLU FFN through cq_moe_ffn, A4W4)
-    and once all in bf16 (torch F.linear).  RMSNorm, rotary embedding and
-    attention (torch scaled_dot_product_attention) are the same torch code in
-    both, in fp16 / bf16.  A third step ("lut_ops") is the LUT one with the norms,
-    residual adds, rotary positions and cache rows through cq_residual_norm (which
-    also makes the QKV product's codes) and cq_rope_qkv; its attention is the same
-    torch call.  Weights are random (the work does not depend on
-    their values); each of the n_layers layers has its own, so a step streams
-    more than the L2.  Both steps are replayed from CUDA graphs."""
+def decoder_layer_steps(cq, M, ctx, n_layers, dev, g):
+    """The three decode steps of decoder_layer_vs_bf16 for M sequences: a dict of
+    functions without arguments, each returning the hidden state [M, H] after the
+    last layer, and the LUT steps' layers (they share weights and KV caches)."""
     import torch
     import torch.nn.functional as F
     H, I, nq, nkv, hd = 2560, 9728, 32, 8, 128
-    g = torch.Generator(device=dev).manual_seed(0)
 
     def rnd_idx(n, k):
         return torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=dev, generator=g)
@@ -745,87 +734,107 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
         o = F.scaled_dot_product_attention(q, kc, vc, enable_gqa=True)
         return o.reshape(M, nq * hd)
 
+    lut_layers, bf_layers = [], []
+    for _ in range(n_layers):
+        nqkv = (nq + 2 * nkv) * hd
+        w = {"sh_gate_idx": rnd_idx(I, H)[None], "sh_up_idx": rnd_idx(I, H)[None],
+             "sh_down_idx": rnd_idx(H, I)[None], "sh_gate_cb": rnd_cb(I)[None],
+             "sh_up_cb": rnd_cb(I)[None], "sh_down_cb": rnd_cb(H)[None]}
+        cfg = cq.MoEConfig(H=H, I=I, E=0, top_k=0, n_shared=1, I_shared=I, act_bits=4,
+                           had_block_h=512, had_block_i=256, had_block_i_shared=256)
+        lut_layers.append(dict(
+            wqkv=rnd_idx(nqkv, H), cqkv=rnd_cb(nqkv), wo=rnd_idx(H, nq * hd), co=rnd_cb(H),
+            ffn=cq.MoELayer(cfg, M, w, dev), w=w,
+            kc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).half(),
+            vc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).half(),
+            n1=torch.ones(H, device=dev), n2=torch.ones(H, device=dev),
+            w1=torch.ones(H, dtype=torch.float16, device=dev),
+            w2=torch.ones(H, dtype=torch.float16, device=dev),
+            y=torch.empty((M, H), dtype=torch.float32, device=dev)))
+        bf_layers.append(dict(
+            wqkv=(torch.randn((nqkv, H), device=dev, generator=g) * 0.02).bfloat16(),
+            wo=(torch.randn((H, nq * hd), device=dev, generator=g) * 0.02).bfloat16(),
+            wgu=(torch.randn((2 * I, H), device=dev, generator=g) * 0.02).bfloat16(),
+            wd=(torch.randn((H, I), device=dev, generator=g) * 0.02).bfloat16(),
+            kc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).bfloat16(),
+            vc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).bfloat16(),
+            n1=torch.ones(H, device=dev), n2=torch.ones(H, device=dev)))
+    x_lut = torch.randn((M, H), device=dev, generator=g).half()
+    x_bf = x_lut.bfloat16()
+
+    def lut_step():
+        x = x_lut
+        for L in lut_layers:
+            qc, sq = cq.cq_rotate_quantize(rms(x, L["n1"]), 512, 4)
+            qkv = cq.cq_lut_gemm(qc, sq, H, 4, L["wqkv"], L["cqkv"])
+            a = attention(qkv, L["kc"], L["vc"], M, torch.float16)
+            oc, so = cq.cq_rotate_quantize(a.contiguous(), 4096, 4)
+            x1 = x + cq.cq_lut_gemm(oc, so, nq * hd, 4, L["wo"], L["co"]).half()
+            L["ffn"](rms(x1, L["n2"]).contiguous(), None, L["y"])
+            x = x1 + L["y"].half()
+        return x
+
+    # the cache's rows as cq_rope_qkv addresses them: token stride hd, head stride
+    # (ctx + 1) hd, sequence m's new token at row m nkv (ctx + 1) + ctx
+    positions = torch.full((M,), ctx, dtype=torch.int32, device=dev)
+    slots = torch.arange(M, device=dev) * (nkv * (ctx + 1)) + ctx
+    freq = torch.from_numpy(cq.rope_inv_freq(hd, 1e6)).to(dev)
+
+    def cache_rows(c):
+        rows = c.numel() // hd - (nkv - 1) * (ctx + 1)
+        return c.as_strided((rows, nkv, hd), (hd, (ctx + 1) * hd, 1))
+
+    def ops_step():
+        r, y = x_lut, None
+        for L in lut_layers:
+            r, _, qc, sq = cq.cq_residual_norm(r, y, pre_weight=L["w1"], had_block=512,
+                                               act_bits=4)
+            qkv = cq.cq_lut_gemm(qc, sq, H, 4, L["wqkv"], L["cqkv"])
+            q, _, _ = cq.cq_rope_qkv(qkv, positions, freq, nq, nkv, head_dim=hd,
+                                     k_out=cache_rows(L["kc"]), v_out=cache_rows(L["vc"]),
+                                     slots=slots)
+            a = F.scaled_dot_product_attention(q.view(M, nq, 1, hd), L["kc"], L["vc"],
+                                               enable_gqa=True)
+            oc, so = cq.cq_rotate_quantize(a.reshape(M, nq * hd), 4096, 4)
+            o = cq.cq_lut_gemm(oc, so, nq * hd, 4, L["wo"], L["co"])
+            r, x1 = cq.cq_residual_norm(r, o, pre_weight=L["w2"])
+            y = L["ffn"](x1, None, L["y"])
+        return r + y.half()
+
+    def bf_step():
+        x = x_bf
+        for L in bf_layers:
+            qkv = F.linear(rms(x, L["n1"]), L["wqkv"])
+            a = attention(qkv, L["kc"], L["vc"], M, torch.bfloat16)
+            x1 = x + F.linear(a, L["wo"])
+            gu = F.linear(rms(x1, L["n2"]), L["wgu"])
+            x = x1 + F.linear(F.silu(gu[:, :I]) * gu[:, I:], L["wd"])
+        return x
+
+    return {"lut": lut_step, "lut_ops": ops_step, "bf16": bf_step}, lut_layers
+
+
+def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers=4):
+    """Decode step of n_layers Qwen3-4B-shaped decoder layers (hidden 2560, 32
+    query / 8 key-value heads of 128, intermediate 9728, a KV cache of ctx
+    tokens per sequence, M sequences decoding one token each), once with the
+    linears as this library's LUT layers (QKV and O through
+    cq_rotate_quantize + cq_lut_gemm, the SwiGLU FFN through cq_moe_ffn, A4W4)
+    and once all in bf16 (torch F.linear).  RMSNorm, rotary embedding and
+    attention (torch scaled_dot_product_attention) are the same torch code in
+    both, in fp16 / bf16.  A third step ("lut_ops") is the LUT one with the norms,
+    residual adds, rotary positions and cache rows through cq_residual_norm (which
+    also makes the QKV product's codes) and cq_rope_qkv; its attention is the same
+    torch call.  Weights are random (the work does not depend on
+    their values); each of the n_layers layers has its own, so a step streams
+    more than the L2.  All three steps are replayed from CUDA graphs."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(0)
     out = {}
     for M in (1, 16):
-        lut_layers, bf_layers = [], []
-        for _ in range(n_layers):
-            nqkv = (nq + 2 * nkv) * hd
-            w = {"sh_gate_idx": rnd_idx(I, H)[None], "sh_up_idx": rnd_idx(I, H)[None],
-                 "sh_down_idx": rnd_idx(H, I)[None], "sh_gate_cb": rnd_cb(I)[None],
-                 "sh_up_cb": rnd_cb(I)[None], "sh_down_cb": rnd_cb(H)[None]}
-            cfg = cq.MoEConfig(H=H, I=I, E=0, top_k=0, n_shared=1, I_shared=I, act_bits=4,
-                               had_block_h=512, had_block_i=256, had_block_i_shared=256)
-            lut_layers.append(dict(
-                wqkv=rnd_idx(nqkv, H), cqkv=rnd_cb(nqkv), wo=rnd_idx(H, nq * hd), co=rnd_cb(H),
-                ffn=cq.MoELayer(cfg, M, w, dev), w=w,
-                kc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).half(),
-                vc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).half(),
-                n1=torch.ones(H, device=dev), n2=torch.ones(H, device=dev),
-                w1=torch.ones(H, dtype=torch.float16, device=dev),
-                w2=torch.ones(H, dtype=torch.float16, device=dev),
-                y=torch.empty((M, H), dtype=torch.float32, device=dev)))
-            bf_layers.append(dict(
-                wqkv=(torch.randn((nqkv, H), device=dev, generator=g) * 0.02).bfloat16(),
-                wo=(torch.randn((H, nq * hd), device=dev, generator=g) * 0.02).bfloat16(),
-                wgu=(torch.randn((2 * I, H), device=dev, generator=g) * 0.02).bfloat16(),
-                wd=(torch.randn((H, I), device=dev, generator=g) * 0.02).bfloat16(),
-                kc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).bfloat16(),
-                vc=torch.randn((M, nkv, ctx + 1, hd), device=dev, generator=g).bfloat16(),
-                n1=torch.ones(H, device=dev), n2=torch.ones(H, device=dev)))
-        x_lut = torch.randn((M, H), device=dev, generator=g).half()
-        x_bf = x_lut.bfloat16()
-
-        def lut_step():
-            x = x_lut
-            for L in lut_layers:
-                qc, sq = cq.cq_rotate_quantize(rms(x, L["n1"]), 512, 4)
-                qkv = cq.cq_lut_gemm(qc, sq, H, 4, L["wqkv"], L["cqkv"])
-                a = attention(qkv, L["kc"], L["vc"], M, torch.float16)
-                oc, so = cq.cq_rotate_quantize(a.contiguous(), 4096, 4)
-                x1 = x + cq.cq_lut_gemm(oc, so, nq * hd, 4, L["wo"], L["co"]).half()
-                L["ffn"](rms(x1, L["n2"]).contiguous(), None, L["y"])
-                x = x1 + L["y"].half()
-            return x
-
-        # the cache's rows as cq_rope_qkv addresses them: token stride hd, head stride
-        # (ctx + 1) hd, sequence m's new token at row m nkv (ctx + 1) + ctx
-        positions = torch.full((M,), ctx, dtype=torch.int32, device=dev)
-        slots = torch.arange(M, device=dev) * (nkv * (ctx + 1)) + ctx
-        freq = torch.from_numpy(cq.rope_inv_freq(hd, 1e6)).to(dev)
-
-        def cache_rows(c):
-            rows = c.numel() // hd - (nkv - 1) * (ctx + 1)
-            return c.as_strided((rows, nkv, hd), (hd, (ctx + 1) * hd, 1))
-
-        def ops_step():
-            r, y = x_lut, None
-            for L in lut_layers:
-                r, _, qc, sq = cq.cq_residual_norm(r, y, pre_weight=L["w1"], had_block=512,
-                                                   act_bits=4)
-                qkv = cq.cq_lut_gemm(qc, sq, H, 4, L["wqkv"], L["cqkv"])
-                q, _, _ = cq.cq_rope_qkv(qkv, positions, freq, nq, nkv, head_dim=hd,
-                                         k_out=cache_rows(L["kc"]), v_out=cache_rows(L["vc"]),
-                                         slots=slots)
-                a = F.scaled_dot_product_attention(q.view(M, nq, 1, hd), L["kc"], L["vc"],
-                                                   enable_gqa=True)
-                oc, so = cq.cq_rotate_quantize(a.reshape(M, nq * hd), 4096, 4)
-                o = cq.cq_lut_gemm(oc, so, nq * hd, 4, L["wo"], L["co"])
-                r, x1 = cq.cq_residual_norm(r, o, pre_weight=L["w2"])
-                y = L["ffn"](x1, None, L["y"])
-            return r, y
-
-        def bf_step():
-            x = x_bf
-            for L in bf_layers:
-                qkv = F.linear(rms(x, L["n1"]), L["wqkv"])
-                a = attention(qkv, L["kc"], L["vc"], M, torch.bfloat16)
-                x1 = x + F.linear(a, L["wo"])
-                gu = F.linear(rms(x1, L["n2"]), L["wgu"])
-                x = x1 + F.linear(F.silu(gu[:, :I]) * gu[:, I:], L["wd"])
-            return x
-
+        steps, _ = decoder_layer_steps(cq, M, ctx, n_layers, dev, g)
         res = {}
-        for nm, fn in (("lut", lut_step), ("lut_ops", ops_step), ("bf16", bf_step)):
+        for nm, fn in steps.items():
             for _ in range(args.warmup):
                 fn()
             torch.cuda.synchronize()
@@ -842,10 +851,10 @@ def decoder_layer_vs_bf16(cq, args, dev, stream, dist, world, ctx=1024, n_layers
                         res["bf16"]["tokens_per_s"],
                         "lut_ops_speedup_vs_bf16": res["lut_ops"]["tokens_per_s"] /
                         res["bf16"]["tokens_per_s"]}
-        del lut_layers, bf_layers
+        del steps, fn
         torch.cuda.empty_cache()
     out["config"] = {"model": "Qwen3-4B-shaped decoder layers (random weights)",
-                     "layers_per_step": n_layers, "kv_context": ctx, "heads": [nq, nkv, hd],
+                     "layers_per_step": n_layers, "kv_context": ctx, "heads": [32, 8, 128],
                      "lut": "A4W4, QKV / O / FFN through the C ABI; attention torch fp16",
                      "lut_ops": "as lut, with cq_residual_norm and cq_rope_qkv",
                      "bf16": "torch F.linear, attention torch bf16"}

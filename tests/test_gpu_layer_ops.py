@@ -762,3 +762,39 @@ def test_refusals_name_the_call_and_the_operand(cq):
         cq.cq_residual_norm(h, eps="small")
     r, x = cq.cq_residual_norm(h)
     assert r is h and (x == 0).all()
+
+
+@pytest.mark.parametrize("M", [1, 5])
+def test_decoder_layer_step_of_the_benchmark_is_the_same_layer(cq, M):
+    """The step with these operators gives the hidden state and the cache rows of the
+    step with torch norms and rotary positions.  They differ by what rounding moves
+    between two int4 codes.  With s the spread of a row, its codes are s / 2 apart:
+    a difference of e s in the row moves a share of 2 e of the codes by one, which
+    is a difference of sqrt(2 e) / 2.  The new k and v rows: x differs by an fp16 step
+    in at most 1 % of the channels (e <= 1e-4): 0.7 %, and 2^-11 of rounding; bound 2 %.
+    The state: that 1 % in the attention's output becomes 7 % of o, which is 0.06 of the
+    state: 0.5 %; 5 % in the gate and up products, 6 % in h, 17 % in the FFN's output,
+    which is 1.2 of a state of 1.6: 13 %; bound 30 %.  Without the FFN's output it
+    would be off by 75 %."""
+    import bench
+    g = torch.Generator(device=DEV).manual_seed(5)
+    ctx = 200
+    steps, layers = bench.decoder_layer_steps(cq, M, ctx, 1, torch.device(DEV), g)
+    L = layers[0]
+    old = L["kc"].clone(), L["vc"].clone()
+    state, rows = {}, {}
+    for nm in ("lut", "lut_ops"):
+        L["kc"].copy_(old[0])
+        L["vc"].copy_(old[1])
+        state[nm] = steps[nm]().double()
+        rows[nm] = [c[:, :, ctx].double() for c in (L["kc"], L["vc"])]
+        assert torch.equal(L["kc"][:, :, :ctx], old[0][:, :, :ctx])
+        assert torch.equal(L["vc"][:, :, :ctx], old[1][:, :, :ctx])
+
+    def off(a, b):
+        return float((a - b).norm() / b.norm())
+
+    assert state["lut"].shape == state["lut_ops"].shape == (M, 2560)
+    assert off(state["lut_ops"], state["lut"]) <= 0.3
+    for a, b, c in zip(rows["lut_ops"], rows["lut"], old):
+        assert off(a, b) <= 0.02 and off(c[:, :, ctx].double(), b) > 0.5
