@@ -5,7 +5,8 @@ ABI declared in include/cq.h.  torch supplies device memory and streams.  The
 operators that a decode step calls between its linears are marshalled by the
 CPython module _cq_bind (csrc/bind.cpp), the others by ctypes.
 There is no CPU fallback: importing this package fails if the library has not
-been built (``python lut_clustered_weight_b200/build.py``).
+been built (``python lut_clustered_weight_b200/build.py``), and the calls that
+_cq_bind marshals fail without it.
 """
 from __future__ import annotations
 
@@ -43,12 +44,36 @@ if not LIB_PATH.exists():
                       "`python lut_clustered_weight_b200/build.py` (nvcc, sm_100a)")
 
 lib = ctypes.CDLL(str(LIB_PATH))
-if not (_PKG / "_cq_bind.so").exists():
-    raise ImportError(f"{_PKG / '_cq_bind.so'} is missing: build it with "
-                      "`python lut_clustered_weight_b200/build.py`")
-from . import _cq_bind as _bind  # noqa: E402
 
-_bind.set_error(CQError)
+
+def _usable_bind(module) -> str | None:
+    """Why a loaded _cq_bind cannot be used, or None: it holds torch's C++ interface,
+    which changes from one torch to the next."""
+    built = getattr(module, "torch_version", None)
+    return None if built == torch.__version__ else (
+        f"it was built for torch {built}, this is {torch.__version__}")
+
+
+class _NoBind:
+    """Stands for a _cq_bind that is missing or of another torch: each call says so."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{_PKG / '_cq_bind.so'} cannot be used: {self._why}; build it with "
+                          "`python lut_clustered_weight_b200/build.py` (g++, torch's headers)")
+
+
+try:
+    from . import _cq_bind as _bind  # noqa: E402
+    _why = _usable_bind(_bind)
+except ImportError as _e:
+    _why = str(_e)
+if _why is None:
+    _bind.set_error(CQError)
+else:
+    _bind = _NoBind(_why)
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 

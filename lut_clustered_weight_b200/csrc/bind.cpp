@@ -401,4 +401,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_cq_bind", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__cq_bind(void) { return PyModule_Create(&g_module); }
+// torch_version: of the torch whose headers this was built with
+PyMODINIT_FUNC PyInit__cq_bind(void) {
+    PyObject *m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", CQ_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

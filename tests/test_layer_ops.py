@@ -1,7 +1,13 @@
 """Operators between two LUT linears, host side: the rotary frequency tables,
 and every argument check of the three C entry points (nothing is launched)."""
 import ctypes
+import importlib.util
 import math
+import os
+import shutil
+import subprocess
+import sys
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -209,3 +215,73 @@ def test_binding_refuses_host_tensors_and_wrong_operands():
         cq.cq_lora_add(h, torch.zeros(2, dtype=torch.int32), h[None], h[None], h.float())
     with pytest.raises(cq.CQError):
         cq.cq_rope_qkv(h.float(), torch.zeros(2, dtype=torch.int32), None, 2, 1, head_dim=16)
+
+
+PKG = Path(cq.__file__).resolve().parent
+
+
+def _python_in(folder, code):
+    env = dict(os.environ, PYTHONPATH=str(folder))
+    return subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env,
+                          cwd=folder, timeout=300)
+
+
+@pytest.mark.parametrize("module", ["absent", "not a library"])
+def test_package_without_the_binding_module_has_everything_else(tmp_path, module):
+    """Only the three calls that it marshals fail, and say how to build it."""
+    to = tmp_path / PKG.name
+    to.mkdir()
+    for f in PKG.glob("*.py"):
+        shutil.copy(f, to)
+    (to / "libcq_b200.so").symlink_to(PKG / "libcq_b200.so")
+    if module != "absent":
+        (to / "_cq_bind.so").write_bytes(b"no library")
+    r = _python_in(tmp_path, f"""
+import {PKG.name} as cq, torch
+assert cq.__file__.startswith({str(tmp_path)!r})
+assert cq.status_string(0) and cq.rope_inv_freq(8).shape == (4,)
+h = torch.zeros((2, 64), dtype=torch.float16)
+n = 0
+for call in (lambda: cq.cq_residual_norm(h), lambda: cq.cq_lora_add(h, h, h, h, h),
+             lambda: cq.cq_rope_qkv(h, h, None, 2, 1, head_dim=16)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_cq_bind" in str(e) and "build.py" in str(e), e
+        n += 1
+assert n == 3
+""")
+    assert r.returncode == 0, r.stderr
+
+
+def test_binding_module_of_another_torch_is_not_used():
+    from types import SimpleNamespace
+    assert cq._usable_bind(SimpleNamespace(torch_version=torch.__version__)) is None
+    for m in (SimpleNamespace(), SimpleNamespace(torch_version="1.0")):
+        assert "torch" in cq._usable_bind(m)
+    assert cq._bind.torch_version == torch.__version__
+
+
+def test_binding_module_is_built_again_for_another_torch_and_left_out_without_a_compiler(
+        tmp_path, monkeypatch):
+    spec = importlib.util.spec_from_file_location("_cq_build_test", PKG / "build.py")
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    assert b.torch_version() == torch.__version__
+    ran = []
+    monkeypatch.setattr(b, "_run", lambda cmd, *a, **k: (ran.append(cmd), Path(
+        cmd[cmd.index("-o") + 1]).write_bytes(b"")))
+    monkeypatch.setattr(b, "BIND", tmp_path / "_cq_bind.so")
+    monkeypatch.setattr(b, "BIND_STAMP", tmp_path / "stamp")
+    b.build_bind()
+    assert len(ran) == 1 and b.BIND.exists()
+    b.build_bind()
+    assert len(ran) == 1                                   # nothing changed
+    monkeypatch.setattr(b, "torch_version", lambda: "9.9")
+    b.build_bind()
+    assert len(ran) == 2
+    monkeypatch.setattr(b.shutil, "which", lambda name: None)
+    monkeypatch.setattr(b, "torch_version", lambda: "9.8")
+    with pytest.warns(UserWarning, match="g[+][+]"):
+        b.build_bind()
+    assert len(ran) == 2
