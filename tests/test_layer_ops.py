@@ -57,6 +57,32 @@ def test_parts_scaling_keeps_fast_and_divides_slow_pairs():
     assert np.allclose(t[mid], plain[mid] * (g + (1 - g) / s), rtol=1e-6, atol=0)
 
 
+@pytest.mark.parametrize("rot,base,s,ctx", [(128, 1e6, 4.0, 32768), (128, 1e4, 16.0, 4096),
+                                            (64, 5e5, 8.0, 8192), (96, 1e4, 2.0, 100)])
+def test_parts_scaling_by_index(rot, base, s, ctx):
+    """Kept up to the last pair that makes 32 turns or more over the context, divided
+    from the first that makes 1 or less, and between these two a line over the index."""
+    t = cq.rope_inv_freq(rot, base, "parts", factor=s, context=ctx, ramp="index").astype(np.float64)
+    plain = [math.exp(-2 * i / rot * math.log(base)) for i in range(rot)]
+    turns = [ctx * f / (2 * math.pi) for f in plain]
+    lo = max([i for i in range(rot) if turns[i] >= 32], default=0)
+    hi = min([i for i in range(rot) if turns[i] <= 1], default=rot - 1)
+    assert hi > lo
+    for i in range(rot // 2):
+        w = min(max((i - lo) / (hi - lo), 0.0), 1.0)
+        assert abs(t[i] / (plain[i] * (1 - w + w / s)) - 1) <= 2.0 ** -23
+    other = cq.rope_inv_freq(rot, base, "parts", factor=s, context=ctx).astype(np.float64)
+    assert np.abs(other / t - 1).max() > 0.1          # the two ramps are different tables
+    assert np.array_equal(other, cq.rope_inv_freq(rot, base, "parts", s, ctx, ramp="turns"))
+
+
+def test_ramp_refusals():
+    parts = dict(rot_dim=8, scaling="parts", factor=2.0, context=4096)
+    for kw in (dict(ramp="other"), dict(ramp="index", base=1.0), dict(ramp="index", slow_turns=0.0)):
+        with pytest.raises(ValueError):
+            cq.rope_inv_freq(**parts, **kw)
+
+
 def test_table_refusals_and_attention_scale():
     for kw in (dict(rot_dim=3), dict(rot_dim=0), dict(rot_dim=8, base=0.0),
                dict(rot_dim=8, factor=0.0), dict(rot_dim=8, scaling="other"),
