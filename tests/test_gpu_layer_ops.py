@@ -259,6 +259,28 @@ def test_residual_norm_scale_of_a_row_beyond_fp16(cq):
     assert np.array_equal(q[[0, 2]], qr) and np.array_equal(s[[0, 2]], sr)
 
 
+@pytest.mark.parametrize("eps", [1e-12, 1e-5, 0.25, 30.0])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_residual_norm_eps_is_the_one_given(cq, kind, eps):
+    """In both norms, in rows of mean squares from 0 to 1e6; codes too."""
+    T, H = 8, 256
+    d = _norm_inputs(T, H, kind, 32, True, True, "none", seed=4)
+    d["y"] *= np.logspace(-4, 2, T, dtype=np.float32)[:, None]
+    d["resid"] *= np.logspace(2, -4, T, dtype=np.float32)[:, None]
+    pw, pb = d["pre"]
+    qw, qb = d["post"]
+    dv = lambda a: None if a is None else _dev(a)  # noqa: E731
+    got = cq.cq_residual_norm(_dev(d["resid"]), _dev(d["y"]), norm=kind, eps=eps, pre_weight=dv(pw),
+                              pre_bias=dv(pb), post_norm=True, post_weight=dv(qw), post_bias=dv(qb),
+                              had_block=64, act_bits=8)
+    f = lambda a: None if a is None else a.astype(np.float64)  # noqa: E731
+    r, x = ref.residual_norm(d["resid"], f(d["y"]), kind, eps, (f(pw), f(pb)), (f(qw), f(qb)), None,
+                             1.0, 1.0)
+    assert np.array_equal(got[0].cpu().numpy(), r) and np.array_equal(got[1].cpu().numpy(), x)
+    qr, sr = oracle.rotate_quantize(x, 64, 8)
+    assert np.array_equal(got[2].cpu().numpy(), qr) and np.array_equal(got[3].cpu().numpy(), sr)
+
+
 # ---------------------------------------------------------------- low-rank adapters
 
 
@@ -387,6 +409,48 @@ def test_lora_add_on_column_slices(cq, M):
         want[:, at:at + N] = sl.cpu().numpy()
         at += N
     assert np.array_equal(buf.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("M", [1, 7, 130, 600, 2100])
+def test_lora_add_from_one_row_stride_to_another(cq, M):
+    """y a slice of rows of one width, out of another; rows with an adapter, with one of
+    rank 0, and without."""
+    K, N = 256, 72
+    g = np.random.default_rng(M)
+    d = _lora_inputs(M, K, N, 4, 16, g.integers(-1, 4, M), seed=M)
+    d["ranks"][2] = 0
+    t = {k: _dev(v) for k, v in d.items()}
+    want = _lora_run(cq, d)
+    y = torch.full((M, N + 40), 3.0, device=DEV)
+    y[:, 16:16 + N] = t["y"]
+    y0 = y.clone()
+    out = torch.full((M, N + 12), 5.0, device=DEV)
+    got = cq.cq_lora_add(t["x"], t["ids"], t["a"], t["b"], y[:, 16:16 + N], scale=t["scale"],
+                         ranks=t["ranks"], out=out[:, 4:4 + N])
+    assert torch.equal(got, want) and torch.equal(y, y0)
+    assert (out[:, :4] == 5).all() and (out[:, 4 + N:] == 5).all()
+    _lora_check(got, d)
+
+
+def test_lora_add_in_a_workspace_of_the_caller(cq):
+    """Calls of different sizes in turn in one buffer, each given exactly the bytes that
+    its size function states: the results of the calls that allocate, and nothing
+    written beside those bytes."""
+    shapes = [(41, 64, 40, 9, 16), (300, 256, 136, 300, 8), (2100, 128, 72, 3, 128),
+              (9000, 16, 24, 5, 8), (256, 2560, 264, 60, 64), (41, 64, 40, 4096, 8)]
+    need = [cq.cq_lora_add_workspace_size(M, n, r) for M, _, _, n, r in shapes]
+    assert min(need) > 0
+    buf = torch.full((max(need) + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    for (M, K, N, n, r), size in list(zip(shapes, need)) * 2:
+        g = np.random.default_rng(M)
+        d = _lora_inputs(M, K, N, n, r, g.integers(-1, n, M), seed=M)
+        want = _lora_run(cq, d)
+        buf.fill_(0xA5)
+        assert torch.equal(_lora_run(cq, d, workspace=buf[256:256 + size]), want)
+        assert (buf[:256] == 0xA5).all() and (buf[256 + size:] == 0xA5).all()
+        with pytest.raises(cq.CQError) as e:
+            _lora_run(cq, d, workspace=buf[256:256 + size - 1])
+        assert e.value.status == cq.CQ_ERR_WORKSPACE
 
 
 @pytest.mark.parametrize("M", [40, 900])
@@ -519,6 +583,25 @@ def test_rope_qkv_against_definition(cq, M, nq, nkv, D, rot, inter, norms, far, 
     for a, b, t in zip(got, want, tol):
         assert a.shape == b.shape
         assert np.all(np.abs(a - b) <= t), float((np.abs(a - b) / t).max())
+
+
+@pytest.mark.parametrize("eps", [1e-12, 1e-2, 5.0])
+def test_rope_qkv_eps_is_the_one_given(cq, eps):
+    """As above: eps is fp32, an input of the same formula."""
+    M, nq, nkv, D = 6, 3, 2, 48
+    g = np.random.default_rng(1)
+    qkv = (g.standard_normal((M, (nq + 2 * nkv) * D)) *
+           np.logspace(-3, 1, M)[:, None]).astype(np.float32)
+    w = [(1 + 0.3 * g.standard_normal(D)).astype(np.float16) for _ in range(2)]
+    pos = np.arange(M, dtype=np.int32)
+    freq = cq.rope_inv_freq(D)
+    got = cq.cq_rope_qkv(_dev(qkv), _dev(pos), _dev(freq), nq, nkv, head_dim=D, q_weight=_dev(w[0]),
+                         k_weight=_dev(w[1]), eps=eps)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    want, tol = ref.rope_qkv(f(qkv), f(pos), f(freq), nq, nkv, D, False, 1.0, f(w[0]), f(w[1]),
+                             float(np.float32(eps)))
+    for a, b, t in zip(got, want, tol):
+        assert np.all(np.abs(ref.f64(a) - b) <= t)
 
 
 def test_rope_qkv_keeps_the_dot_product_of_equal_distances(cq):

@@ -172,6 +172,18 @@ def test_lora_add_workspace():
     assert cq.cq_lora_add_workspace_size(-1, 4, 16) == 0
 
 
+def test_lora_add_workspace_is_asked_for_above_40_rows():
+    for M in (41, 64, 4096, 1 << 20):
+        for n in (1, 4096):
+            need = cq.cq_lora_add_workspace_size(M, n, 16)
+            # the sorted rows' t in two fp16 parts, their factors, their list
+            assert need >= M * (2 * 16 * 2 + 4 + 4)
+            assert need < cq.cq_lora_add_workspace_size(2 * M, n, 16)
+            assert need < cq.cq_lora_add_workspace_size(M, n, 128)
+    for M in (1, 40):
+        assert cq.cq_lora_add_workspace_size(M, 8, 16) == 0
+
+
 # ---------------------------------------------------------------- cq_rope_qkv
 
 
