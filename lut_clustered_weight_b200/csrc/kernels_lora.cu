@@ -2,19 +2,24 @@
 // shared projection, sm_100a.  out = y + scale * B (A x) with the adapter of
 // each row.
 //
-// Rows of one adapter are gathered into tiles of up to TM rows; a cluster of
-// CTAs works on a tile in one launch:
-//   shrink  t = A x: the cluster's CTAs, and the warps of a CTA, split K; the
+// Rows of one adapter are gathered into tiles of up to TM rows.  A tile's work is
+//   shrink  t = A x: the CTAs of a cluster, and the warps of a CTA, split K; the
 //           partial t are summed through shared and distributed shared memory
-//           in a fixed order, so every CTA of the cluster has all of t
-//   expand  out = y + scale * B t: the CTAs split the columns
-// so t never goes to global memory and every CTA streams its part of A, x, B
-// and y once.  Both products run on mma.sync m16n8k16: the op is bound by bytes (y
-// is read and written in fp32), not by the tensor pipe (at rank 64 it does 16
-// flops a byte).  The shrink's operands come by cp.async through a ring of stages,
-// so that a CTA's whole part of K is on its way at once; the expansion's straight
-// from global memory into fragments: a lane takes 16 bytes (8 consecutive k) of a
-// row of B, which serves two k16 steps when both operands are permuted along k alike.
+//           in a fixed order
+//   expand  out = y + scale * B t: CTAs split the columns
+// in one of two forms (lora_one_launch):
+//   one launch (k_lora; up to 40 rows, and up to 256 where the work is small): every CTA
+//           finds its tile in the ids, a cluster does both products of a tile and t stays
+//           in its shared memory; B goes straight from global memory into fragments: a
+//           lane takes 16 bytes (8 consecutive k) of a row of B, which serves two k16 steps
+//           when both operands are permuted along k alike
+//   planned (k_lora_plan, k_lora_t, k_lora_out): one CTA sorts the rows into tiles of the
+//           workspace, clusters write t there, and the columns are a launch of their own,
+//           with B and y through a ring of shared-memory stages
+// Either way A, x, B and y are streamed once per tile, the shrink's operands by cp.async
+// through a ring of stages, so that a CTA's part of K is on its way at once.  Both products
+// run on mma.sync m16n8k16: the op is bound by bytes (y is read and written in fp32),
+// not by the tensor pipe (at rank 64 it does 16 flops a byte).
 //
 // t is fp32 and B is fp16: t is scaled by a power of two per row, so that its
 // largest entry is in [1, 2), and split into two fp16 parts, t = hi + lo with
@@ -983,7 +988,11 @@ k_lora_plan(const int32_t *__restrict__ ids, int M, int n, int TM, bool skip_non
 static bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Rows of a tile: 16 (one MMA row block) while there are few, 64 for batches of
-// many rows, where A and B are then re-read a quarter as often.
+// many rows, where A and B are then re-read a quarter as often.  Measured, us, 16 and 64:
+// K 2048, N 2816, 8 adapters of rank 64: 600 rows 15.0 and 17.3, 1500: 25.1 and 20.6, 3000:
+// 42.7 and 33.2, 4096: 49.8 and 33.9; K = N = 4096, 16 of rank 16: 1024 rows 17.3 and 20.7,
+// 2048: 24.4 and 29.1, 3000: 39.0 and 38.3; K 1024, N 2048, 4 of rank 128: 1024 rows 19.2
+// and 19.3, 4096: 56.5 and 37.5.  The two cross between 1024 and 3000 rows.
 static int lora_tile_rows(int64_t M) { return M >= 2048 ? 64 : 16; }
 static int64_t lora_max_tiles(int64_t M, int64_t n) {
     return M / lora_tile_rows(M) + std::min(n + 1, M);
@@ -1036,7 +1045,9 @@ static cudaError_t launch_planned(LoraArgs p, cudaStream_t st) {
     cudaError_t e = launch_pdl(k_lora_t<TM, R>, dim3((unsigned)(tiles * C)), dim3(kLoraThreads),
                                (size_t)LoraShape<TM, R>::pool, st, C, p);
     if (e != cudaSuccess) return e;
-    // column shares of a tile: two CTAs an SM in all, of at least four steps each
+    // column shares of a tile: two CTAs an SM in all, of at least four steps each (a share
+    // of fewer fills its ring for little: 517 rows, N 2560, rank 32 16.7 us, and 18.3 with
+    // one step or two; of eight 19.6: too few CTAs)
     using S = OutShape<TM, R>;
     const int nblk = (p.N + S::W - 1) / S::W;
     const int64_t full = std::max<int64_t>(1, p.M / TM);

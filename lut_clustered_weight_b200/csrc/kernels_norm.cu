@@ -333,6 +333,12 @@ CQ_DEV uint32_t nibbles(uint32_t a) {
     return a | a >> 4;  // bytes 0 and 2 hold the pairs
 }
 
+// A later row's bytes, into the L2
+CQ_DEV void prefetch_row(const void *p, int bytes, int j, int threads) {
+    for (int i = 128 * j; i < bytes; i += 128 * threads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p) + i));
+}
+
 // Rows in registers, E channels a thread.  The rotation's index bits are taken
 // log2 E at a time: the lowest in the layout of the loads, each further group
 // after an exchange through shared memory that puts the group's 2^N values into
@@ -341,12 +347,6 @@ CQ_DEV uint32_t nibbles(uint32_t a) {
 // come first and the second, [log2 E, ..), last, so the codes are made in one of
 // few layouts; they go through shared memory once, as bytes, back to the layout
 // of the loads.
-// A later row's bytes, into the L2
-CQ_DEV void prefetch_row(const void *p, int bytes, int j, int threads) {
-    for (int i = 128 * j; i < bytes; i += 128 * threads)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p) + i));
-}
-
 template <int E, int REGS, bool R16, bool CODES>
 __global__ void __maxnreg__(REGS) k_residual_norm(const NormArgs a) {
     extern __shared__ __align__(16) double xch_all[];
@@ -559,7 +559,7 @@ template <int E, int REGS>
 static cudaError_t launch_rows(NormArgs a, bool r16, cudaStream_t st) {
     const int T = (a.H + E - 1) / E;
     a.tpr = (T + 31) / 32 * 32;
-    // short rows share a CTA of up to 256 threads
+    // short rows share a CTA of up to 128 threads
     a.rpc = (int)std::min<int64_t>(std::max(1, 128 / a.tpr), a.T);
     const bool codes = a.bits > 0;
     // A row fetches the one that takes its place where the arithmetic is short (4096 rows of

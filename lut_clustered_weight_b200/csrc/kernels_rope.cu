@@ -65,12 +65,12 @@ CQ_DEV void load_unit(RopeUnit &u, const RopeArgs &p, const float *row, int h, i
     }
 }
 
-// Memory-bound where tokens are many: 4096 of 32 + 8 heads of 128 in 28.5 us, 0.82 of a
-// copy's bandwidth (32.6 with the norms, which add shuffles); one token 2 us.  PACKED:
-// the units of all heads follow one another (width D / 8, not a power of two; 4096 tokens
-// of 24 + 8 heads of 80: 16.9 us, and 21.1 in groups of 16 lanes).  The layout and the
-// norm are template parameters: with all of them read at run time it was bound by
-// instructions (29.2 us).
+// Memory-bound where tokens are many: 4096 of 32 + 8 heads of 128 in 28.3 us, 0.82 of a
+// copy's bandwidth; 33.2 with the norms, whose sum is a chain of shuffles per round, of 4 at
+// this width; one token 2 us.  PACKED: the units of all heads follow one another (width
+// D / 8, not a power of two; 4096 tokens of 24 + 8 heads of 80: 16.9 us, and 21.1 in groups
+// of 16 lanes).  The layout and the norm are template parameters: with all of them read at
+// run time it was bound by instructions (29.2 us).
 template <bool NORM, bool INTER, bool PACKED>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
     __shared__ float2 cs[kRopeMaxDim / 2];
@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_qkv(const RopeArgs p) {
         cs[i] = make_float2(c * p.attn_scale, s * p.attn_scale);
     }
     __syncthreads();
-    // every thread runs the same rounds (the shuffles need all lanes); h0: the head of
-    // the round's first unit or one before it
+    // every thread runs the same rounds (the shuffles need all lanes); h0: at or before the
+    // head of the round's first unit (packed units move on by step_u more a round; the
+    // rounds past the last head find no live unit)
     for (int h0 = h_begin; h0 < h_end; h0 += p.step_h) {
         const RopeUnit u = next;
         nh += p.step_h;
