@@ -412,7 +412,9 @@ class MoELayer:
 
 
 # ---------------------------------------------------------------------------
-# the operators between two LUT linears of a decoder layer
+# the operators between two LUT linears of a decoder layer.  stream: a torch stream, its
+# address, or None (the current one); the outputs and workspaces that a call allocates
+# belong to its stream, as if allocated with that stream current.
 
 
 NORM_KINDS = {"rms": 0, "layer": 1}   # cq_norm_kind
